@@ -6,9 +6,11 @@ CUDA stream to the C ABI (include/blockffn.h).  All arithmetic runs in the
 library's kernels; PyTorch only provides device memory and streams.
 """
 from .api import (BlockFFNError, Workspace, chunk_union, debug_set_trace, debug_skip_flag, device_status,
-                  forward,
-                  num_sms, residual_layernorm, route, set_wait_limit_ns, version, workspace_bytes)
+                  forward, int8_linear,
+                  num_sms, quantize_int8, residual_layernorm, route, route_topk, route_topk_backward,
+                  set_wait_limit_ns, version, workspace_bytes)
 
 __all__ = ["BlockFFNError", "Workspace", "chunk_union", "debug_set_trace", "debug_skip_flag", "residual_layernorm",
            "device_status",
-           "forward", "num_sms", "route", "set_wait_limit_ns", "version", "workspace_bytes"]
+           "forward", "int8_linear", "num_sms", "quantize_int8", "route", "route_topk", "route_topk_backward",
+           "set_wait_limit_ns", "version", "workspace_bytes"]

@@ -49,6 +49,15 @@ SIGNATURES = {
                                  c_void_p, c_void_p, c_void_p,
                                  c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_int, c_int,
                                  c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "blockffn_route_topk": (c_int, [c_void_p, c_int, c_void_p, c_int, c_int, c_int, c_int, c_int,
+                                    c_int, c_int, c_float, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "blockffn_route_topk_backward": (c_int, [c_void_p, c_int, c_void_p, c_void_p, c_int, c_int,
+                                             c_int, c_int, c_int, c_float, c_void_p, c_void_p]),
+    "blockffn_quantize_int8": (c_int, [c_void_p, c_int, c_int, c_int, c_void_p, c_void_p,
+                                       c_void_p]),
+    "blockffn_int8_linear_workspace_bytes": (c_size_t, [c_int, c_int, c_int]),
+    "blockffn_int8_linear": (c_int, [c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_int, c_int,
+                                     c_int, c_int, c_void_p, c_void_p, c_size_t, c_void_p]),
     "blockffn_get_device_status": (c_int, [c_void_p, c_void_p, c_int32_p]),
     "blockffn_forward_noalloc": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int,
                                          c_int, c_int, c_int, c_void_p, c_void_p]),
@@ -66,5 +75,7 @@ for _name, (_res, _args) in SIGNATURES.items():
 # status codes and dtypes (include/blockffn.h)
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT, ERR_WORKSPACE = range(6)
 F32, BF16 = 0, 1
+# scores of the top-k router
+SOFTMAX, SIGMOID = 0, 1
 # workspace-size flags
 WS_ROUTER, WS_EXPERT_BIAS = 1, 2

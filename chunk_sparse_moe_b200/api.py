@@ -132,8 +132,15 @@ class Workspace:
         return self.buf.numel()
 
     def reset(self) -> None:
-        _check(lib.blockffn_workspace_reset(self.buf.data_ptr(), self.nbytes, _stream()),
-               "blockffn_workspace_reset")
+        _launch("blockffn_workspace_reset", lib.blockffn_workspace_reset, self.buf.device, self.buf.data_ptr(),
+                self.nbytes)
+
+    @classmethod
+    def for_int8_linear(cls, T: int, K: int, O: int, device=None) -> "Workspace":
+        nb = int(lib.blockffn_int8_linear_workspace_bytes(T, K, O))
+        if nb == 0:
+            raise BlockFFNError(_lib.ERR_INVALID_ARG, "blockffn_int8_linear_workspace_bytes")
+        return cls(nb, device)
 
     @classmethod
     def for_shapes(cls, T, d_h, E, d_e, n, dtype, with_router, device=None,
@@ -177,6 +184,129 @@ def forward(x: torch.Tensor, W_in: torch.Tensor, W_out: torch.Tensor, n: int,
                               _ptr(W_in), _ptr(W_out), T, d_h, E, d_e, n, _dtype_code(x), opts,
                               _ptr(y), workspace.buf.data_ptr(), workspace.nbytes, _stream())
     _check(st, "blockffn_forward")
+    return y
+
+
+# ------------------------------------------------ top-k routing, 8-bit products --
+_SCORES = {"softmax": _lib.SOFTMAX, "sigmoid": _lib.SIGMOID}
+
+
+def _scores_code(scores: str) -> int:
+    if scores not in _SCORES:
+        raise ValueError(f"scores must be 'softmax' or 'sigmoid', not {scores!r}")
+    return _SCORES[scores]
+
+
+def _want(t: torch.Tensor, what: str, dtype, shape, device) -> torch.Tensor:
+    """``t`` itself, once its type, shape and device are as they have to be."""
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{what}: on {t.device}, expected {device}")
+    return t
+
+
+def _launch(where: str, fn, device: torch.device, *args) -> None:
+    """Call ``fn(*args, stream)`` with the tensors' device current, on its current stream."""
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream()), where)
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream()), where)
+
+
+def route_topk(logits: torch.Tensor, k: int, scores: str = "softmax", bias: Optional[torch.Tensor] = None,
+               n_group: int = 1, topk_group: Optional[int] = None, renormalize: bool = True, scale: float = 1.0,
+               out=None):
+    """Top-k routing of router logits [T, E] (fp32 or bf16): (gates [T, E] fp32, ids [T, k]
+    int32, weights [T, k] fp32).
+
+    The k experts of largest score (``scores``: "softmax" over the experts or "sigmoid"
+    of each) plus ``bias`` [E] fp32, out of the ``topk_group`` best of ``n_group`` groups
+    of neighbouring experts (a group counts the sum of its two best); weights are the
+    chosen scores without the bias, divided by their sum when ``renormalize`` is set,
+    times ``scale``.  ``gates`` holds them densely, as ``chunk_union`` and the forwards
+    take them.  Ties go to the lowest index; an expert whose logit is -inf is never
+    chosen (ids -1 and weight 0 where too few are left).  ``out``: the three outputs."""
+    T, E = logits.shape
+    dev = logits.device
+    if bias is not None:
+        _want(bias, "bias", torch.float32, (E,), dev)
+    if out is None:
+        gates = torch.empty((T, E), dtype=torch.float32, device=dev)
+        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+        weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    else:
+        gates, ids, weights = out
+        _want(gates, "gates", torch.float32, (T, E), dev)
+        _want(ids, "ids", torch.int32, (T, k), dev)
+        _want(weights, "weights", torch.float32, (T, k), dev)
+    _launch("blockffn_route_topk", lib.blockffn_route_topk, dev, _ptr(logits), _dtype_code(logits), _ptr(bias),
+            T, E, k, _scores_code(scores), n_group, n_group if topk_group is None else topk_group,
+            int(bool(renormalize)), float(scale), _ptr(gates), _ptr(ids), _ptr(weights))
+    return gates, ids, weights
+
+
+def route_topk_backward(logits: torch.Tensor, ids: torch.Tensor, d_weights: torch.Tensor, scores: str = "softmax",
+                        renormalize: bool = True, scale: float = 1.0,
+                        d_logits: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient [T, E] (the logits' type) of ``route_topk``'s weights with respect to the
+    logits, the choice ``ids`` held fixed, for ``d_weights`` [T, k] fp32."""
+    T, E = logits.shape
+    dev = logits.device
+    k = ids.shape[-1]
+    _want(ids, "ids", torch.int32, (T, k), dev)
+    _want(d_weights, "d_weights", torch.float32, (T, k), dev)
+    if d_logits is None:
+        d_logits = torch.empty_like(logits)
+    else:
+        _want(d_logits, "d_logits", logits.dtype, (T, E), dev)
+    _launch("blockffn_route_topk_backward", lib.blockffn_route_topk_backward, dev, _ptr(logits), _dtype_code(logits),
+            _ptr(ids), _ptr(d_weights), T, E, k, _scores_code(scores), int(bool(renormalize)), float(scale),
+            _ptr(d_logits))
+    return d_logits
+
+
+def quantize_int8(w: torch.Tensor):
+    """(q int8 of w's shape, scale fp32 of w's shape without the last axis): every row of
+    the last axis in 8 bits, w about q * scale.  Lays out weights for the 8-bit
+    products: [O, K] for ``int8_linear``, [E, d_e, d_h] and [E, d_h, d_e] for
+    ``forward_int8``."""
+    if w.dim() < 1 or w.shape[-1] < 1:
+        raise ValueError(f"w: shape {tuple(w.shape)} has no rows to round")
+    cols = w.shape[-1]
+    rows = w.numel() // cols
+    q = torch.empty(w.shape, dtype=torch.int8, device=w.device)
+    scale = torch.empty(w.shape[:-1], dtype=torch.float32, device=w.device)
+    _launch("blockffn_quantize_int8", lib.blockffn_quantize_int8, w.device, _ptr(w), rows, cols, _dtype_code(w),
+            _ptr(q), _ptr(scale))
+    return q, scale
+
+
+def int8_linear(x: torch.Tensor, W: torch.Tensor, s_w: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                out_dtype: Optional[torch.dtype] = None, y: Optional[torch.Tensor] = None,
+                workspace: Optional[Workspace] = None) -> torch.Tensor:
+    """y [T, O] = x W^T in 8-bit integers: x [T, K] (fp32 or bf16) is rounded to 8 bits with
+    a scale for each token, W [O, K] int8 has the scales ``s_w`` [O] fp32
+    (``quantize_int8``), ``bias`` [O] fp32 is optional.  ``out_dtype``: fp32 or bf16
+    (default: x's)."""
+    T, K = x.shape
+    O = W.shape[0]
+    dev = x.device
+    _want(W, "W", torch.int8, (O, K), dev)
+    _want(s_w, "s_w", torch.float32, (O,), dev)
+    if bias is not None:
+        _want(bias, "bias", torch.float32, (O,), dev)
+    if y is None:
+        y = torch.empty((T, O), dtype=out_dtype or x.dtype, device=dev)
+    else:
+        _want(y, "y", out_dtype or y.dtype, (T, O), dev)
+    if workspace is None:
+        workspace = Workspace.for_int8_linear(T, K, O, dev)
+    _launch("blockffn_int8_linear", lib.blockffn_int8_linear, dev, _ptr(x), _dtype_code(x), _ptr(W), _ptr(s_w),
+            _ptr(bias), T, K, O, _dtype_code(y), _ptr(y), _ptr(workspace.buf), workspace.nbytes)
     return y
 
 

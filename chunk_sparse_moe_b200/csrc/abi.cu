@@ -132,6 +132,20 @@ bool make_map_plain(CUtensorMap* m, const void* base, uint64_t inner, uint64_t o
               CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 2-D tensor of bytes [outer, inner], box {128, box_outer}, 128-byte swizzle
+// (inner a multiple of 16).
+bool make_map_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint32_t box_outer) {
+    auto fn = encode_fn();
+    if (fn == nullptr) return false;
+    cuuint64_t dims[2] = {inner, outer};
+    cuuint64_t strides[1] = {inner};
+    cuuint32_t box[2] = {128, box_outer};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Which kernel computes a forward call.
 enum class Path { F32, Decode, Group };
 
@@ -320,6 +334,141 @@ blockffn_status blockffn_chunk_union(const float* gates, int T, int E, int n, in
     if (!gates || !counts || !idx || !tmask) return fail(BLOCKFFN_ERR_INVALID_ARG, "null pointer");
     cudaError_t e = launch_chunk_union(gates, T, E, n, counts, idx, tmask, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? BLOCKFFN_OK : cuda_fail(e, "chunk_union launch");
+}
+
+blockffn_status blockffn_route_topk(const void* logits, blockffn_dtype dt, const float* bias, int T, int E, int k,
+                                    blockffn_scores scores, int n_group, int topk_group, int renormalize,
+                                    float scale, float* gates, int32_t* ids, float* weights, void* stream) {
+    if (dt != BLOCKFFN_F32 && dt != BLOCKFFN_BF16) return fail(BLOCKFFN_ERR_INVALID_ARG, "unknown dtype %d", (int)dt);
+    if (scores != BLOCKFFN_SOFTMAX && scores != BLOCKFFN_SIGMOID)
+        return fail(BLOCKFFN_ERR_INVALID_ARG, "unknown scores %d", (int)scores);
+    if (T < 0 || E < 1 || E > 256) return fail(BLOCKFFN_ERR_INVALID_ARG, "bad shape (T = %d, E = %d)", T, E);
+    if (n_group < 1 || E % n_group != 0)
+        return fail(BLOCKFFN_ERR_INVALID_ARG, "%d groups do not divide E = %d", n_group, E);
+    if (topk_group < 1 || topk_group > n_group)
+        return fail(BLOCKFFN_ERR_INVALID_ARG, "topk_group = %d outside [1, %d]", topk_group, n_group);
+    if (k < 1 || k > 32 || k > topk_group * (E / n_group))
+        return fail(BLOCKFFN_ERR_INVALID_ARG, "k = %d outside [1, min(32, %d experts of the chosen groups)]", k,
+                    topk_group * (E / n_group));
+    if (!std::isfinite(scale)) return fail(BLOCKFFN_ERR_INVALID_ARG, "scale must be finite");
+    if (T == 0) return BLOCKFFN_OK;
+    if (!logits || !ids || !weights) return fail(BLOCKFFN_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(logits) || !aligned16(ids) || !aligned16(weights) || (bias && !aligned16(bias)) ||
+        (gates && !aligned16(gates)))
+        return fail(BLOCKFFN_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
+    cudaError_t e = launch_route_topk(logits, dt == BLOCKFFN_BF16, bias, T, E, k, scores == BLOCKFFN_SIGMOID, n_group,
+                                      topk_group, renormalize != 0, scale, gates, ids, weights,
+                                      static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? BLOCKFFN_OK : cuda_fail(e, "route_topk launch");
+}
+
+blockffn_status blockffn_route_topk_backward(const void* logits, blockffn_dtype dt, const int32_t* ids,
+                                             const float* d_weights, int T, int E, int k, blockffn_scores scores,
+                                             int renormalize, float scale, void* d_logits, void* stream) {
+    if (dt != BLOCKFFN_F32 && dt != BLOCKFFN_BF16) return fail(BLOCKFFN_ERR_INVALID_ARG, "unknown dtype %d", (int)dt);
+    if (scores != BLOCKFFN_SOFTMAX && scores != BLOCKFFN_SIGMOID)
+        return fail(BLOCKFFN_ERR_INVALID_ARG, "unknown scores %d", (int)scores);
+    if (T < 0 || E < 1 || E > 256) return fail(BLOCKFFN_ERR_INVALID_ARG, "bad shape (T = %d, E = %d)", T, E);
+    if (k < 1 || k > 32 || k > E) return fail(BLOCKFFN_ERR_INVALID_ARG, "k = %d outside [1, min(32, E)]", k);
+    if (!std::isfinite(scale)) return fail(BLOCKFFN_ERR_INVALID_ARG, "scale must be finite");
+    if (T == 0) return BLOCKFFN_OK;
+    if (!logits || !ids || !d_weights || !d_logits) return fail(BLOCKFFN_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(logits) || !aligned16(ids) || !aligned16(d_weights) || !aligned16(d_logits))
+        return fail(BLOCKFFN_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
+    cudaError_t e = launch_route_topk_backward(logits, dt == BLOCKFFN_BF16, ids, d_weights, T, E, k,
+                                               scores == BLOCKFFN_SIGMOID, renormalize != 0, scale, d_logits,
+                                               static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? BLOCKFFN_OK : cuda_fail(e, "route_topk_backward launch");
+}
+
+blockffn_status blockffn_quantize_int8(const void* w, int rows, int cols, blockffn_dtype dt, int8_t* q, float* scale,
+                                       void* stream) {
+    if (dt != BLOCKFFN_F32 && dt != BLOCKFFN_BF16) return fail(BLOCKFFN_ERR_INVALID_ARG, "unknown dtype %d", (int)dt);
+    if (rows < 0 || cols < 1 || cols > (1 << 26))
+        return fail(BLOCKFFN_ERR_INVALID_ARG, "bad shape (%d rows of %d)", rows, cols);
+    if (rows == 0) return BLOCKFFN_OK;
+    if (!w || !q || !scale) return fail(BLOCKFFN_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(w) || !aligned16(q) || !aligned16(scale))
+        return fail(BLOCKFFN_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
+    cudaError_t e = launch_quantize_rows(w, dt == BLOCKFFN_BF16, rows, cols, q, scale,
+                                         static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? BLOCKFFN_OK : cuda_fail(e, "quantize_int8 launch");
+}
+
+namespace {
+
+blockffn_status check_int8_linear(int T, int K, int O) {
+    if (T < 0 || K < 1 || O < 1) return fail(BLOCKFFN_ERR_INVALID_ARG, "bad shape (T = %d, K = %d, O = %d)", T, K, O);
+    if (K % 16 != 0) return fail(BLOCKFFN_ERR_UNSUPPORTED, "int8_linear needs K %% 16 == 0 (K = %d)", K);
+    // the int32 sums of K products of at most 127 * 127 (128 * 128 for a weight of -128)
+    if (K > 131056) return fail(BLOCKFFN_ERR_UNSUPPORTED, "int8_linear: K = %d above 131056 (int32 sums)", K);
+    if (((long long)T + 15) / 16 * (((long long)O + 127) / 128) > 0x7fffffffLL / 8)
+        return fail(BLOCKFFN_ERR_UNSUPPORTED, "int8_linear: T * O too large");
+    return BLOCKFFN_OK;
+}
+
+// workspace of int8_linear: control block, token scales, the tokens' 8-bit rows
+struct LinearLayout {
+    size_t sx, q, total;
+};
+LinearLayout linear_layout(int T, int K) {
+    LinearLayout L;
+    L.sx = sizeof(Ctl);
+    L.q = align_up(L.sx + (size_t)T * 4, 256);
+    L.total = align_up(L.q + (size_t)T * K, 256);
+    return L;
+}
+
+}  // namespace
+
+size_t blockffn_int8_linear_workspace_bytes(int T, int K, int O) {
+    if (check_int8_linear(T, K, O) != BLOCKFFN_OK) return 0;
+    return linear_layout(T, K).total;
+}
+
+blockffn_status blockffn_int8_linear(const void* x, blockffn_dtype dt, const int8_t* W, const float* s_w,
+                                     const float* bias, int T, int K, int O, blockffn_dtype y_dt, void* y,
+                                     void* workspace, size_t ws_bytes, void* stream) {
+    if ((dt != BLOCKFFN_F32 && dt != BLOCKFFN_BF16) || (y_dt != BLOCKFFN_F32 && y_dt != BLOCKFFN_BF16))
+        return fail(BLOCKFFN_ERR_INVALID_ARG, "unknown dtype (%d, %d)", (int)dt, (int)y_dt);
+    blockffn_status st = check_int8_linear(T, K, O);
+    if (st != BLOCKFFN_OK) return st;
+    if (T == 0) return BLOCKFFN_OK;
+    if (!x || !W || !s_w || !y || !workspace) return fail(BLOCKFFN_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(x) || !aligned16(W) || !aligned16(s_w) || !aligned16(y) || !aligned16(workspace) ||
+        (bias && !aligned16(bias)))
+        return fail(BLOCKFFN_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
+    const LinearLayout L = linear_layout(T, K);
+    if (ws_bytes < L.total)
+        return fail(BLOCKFFN_ERR_WORKSPACE, "workspace of %zu bytes < %zu needed", ws_bytes, L.total);
+    const int G = num_sms_current();
+    if (G <= 0) return fail(BLOCKFFN_ERR_CUDA, "no current CUDA device");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    char* ws = static_cast<char*>(workspace);
+    int8_t* q = reinterpret_cast<int8_t*>(ws + L.q);
+    float* sx = reinterpret_cast<float*>(ws + L.sx);
+    IlArgs a;
+    a.sx = sx;
+    a.sw = s_w;
+    a.bias = bias;
+    a.y = y;
+    a.ctl = reinterpret_cast<Ctl*>(ws);
+    a.T = T;
+    a.O = O;
+    a.KB = (K + 127) / 128;
+    int8_linear_plan(T, K, O, G, &a.N, &a.S);
+    a.tiles_o = (O + 127) / 128;
+    a.tiles_t = (T + a.N - 1) / a.N;
+    a.stages = 0;
+    a.wait_ns = g_wait_ns.load();
+    CUtensorMap maps[2];
+    if (!make_map_u8(&maps[0], W, (uint64_t)K, (uint64_t)O, 128) ||
+        !make_map_u8(&maps[1], q, (uint64_t)K, (uint64_t)T, (uint32_t)a.N))
+        return fail(BLOCKFFN_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+    cudaError_t e = launch_quantize_rows(x, dt == BLOCKFFN_BF16, T, K, q, sx, s);
+    if (e != cudaSuccess) return cuda_fail(e, "quantize launch");
+    e = launch_int8_linear(a, maps, y_dt == BLOCKFFN_BF16, G, s);
+    return e == cudaSuccess ? BLOCKFFN_OK : cuda_fail(e, "int8_linear launch");
 }
 
 size_t blockffn_forward_workspace_bytes(int T, int d_h, int E, int d_e, int n, blockffn_dtype dt, int flags) {

@@ -1,0 +1,363 @@
+// int8_linear.cu -- rows rounded to 8 bits, and the product of 8-bit integers with a
+// scale for each token and each output channel on the sm_100a tensor cores.
+//
+//   q_t  = rint(127 x_t / amax_t),  s_t = amax_t / 127            (quantize kernel)
+//   y[t, o] = s_t s_w[o] (sum_k q[t, k] W[o, k]) + bias[o]        (product kernel)
+//
+// The sums are exact: int8 x int8 into int32 (tcgen05 kind::i8), so the order of
+// the K blocks, and how K is split, do not matter.  int32 -> fp32, the two scales
+// and the bias are the only roundings before the one to y's type.
+//
+// Tiles.  128 output channels (M, the weight's rows) by N tokens (N = 16 .. 256):
+// the weight is the operand that a small batch streams, so it fills the MMA's M
+// whatever T is.  A pipeline stage is 128 bytes of K of both operands, brought by
+// TMA in the 128-byte swizzle the MMA reads; K's tail and the rows behind O and T
+// are zeros that TMA fills in.
+//
+// Few tiles: a cluster of S blocks shares a tile, each multiplying a slice of K.  The
+// int32 partial sums stay in each block's shared memory; after a cluster barrier
+// each block adds N / S token columns over the S blocks.  Many tiles: one
+// persistent block per SM, two accumulators in TMEM, so the epilogue of a tile runs
+// under the MMAs of the next.
+//
+// Roles (384 threads): warp 0 loads, warp 1 issues the MMAs, warp 2 owns TMEM,
+// warps 4-11 are the epilogue (a thread is one channel; two groups of four
+// warps take alternate 16-column pieces).  The product kernel is a programmatic
+// dependent of the quantize kernel: the weights' first tiles are loaded while that
+// one still runs.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "int8.cuh"
+#include "launch.h"
+
+namespace bffn {
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const T* __restrict__ v, int K, int8_t* __restrict__ q,
+                                                            float* __restrict__ scale) {
+    __shared__ uint32_t red[8];
+    griddep_wait();
+    griddep_launch_dependents();
+    const size_t row = blockIdx.x;
+    quantize_row<T, VEC>(v + row * K, K, q + row * K, scale + row, red);
+}
+
+cudaError_t launch_quantize_rows(const void* v, bool bf16, int rows, int K, int8_t* q, float* scale, cudaStream_t s) {
+    const int eb = bf16 ? 2 : 4;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)rows);
+    cfg.blockDim = dim3((unsigned)quantize_threads(K, eb));
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const bool one = quantize_one_pass(K, eb);
+    if (bf16) {
+        auto* p = static_cast<const __nv_bfloat16*>(v);
+        return one ? cudaLaunchKernelEx(&cfg, quantize_rows_kernel<__nv_bfloat16, true>, p, K, q, scale)
+                   : cudaLaunchKernelEx(&cfg, quantize_rows_kernel<__nv_bfloat16, false>, p, K, q, scale);
+    }
+    auto* p = static_cast<const float*>(v);
+    return one ? cudaLaunchKernelEx(&cfg, quantize_rows_kernel<float, true>, p, K, q, scale)
+               : cudaLaunchKernelEx(&cfg, quantize_rows_kernel<float, false>, p, K, q, scale);
+}
+
+namespace {
+
+constexpr int kIlThreads = 384;
+constexpr int kIlMaxStages = 12;
+constexpr int kIlABytes = 128 * 128;          // weight tile: 128 rows x 128 int8
+constexpr int kIlRing = 200 * 1024;           // shared memory of the stages
+
+struct IlShared {
+    uint64_t full[kIlMaxStages];
+    uint64_t empty[kIlMaxStages];
+    uint64_t acc_full[2];
+    uint64_t acc_empty[2];
+    uint64_t mma_done;
+    uint32_t tmem_base;
+    volatile int abort;
+};
+
+__device__ __forceinline__ void il_put(float* y, float v) { *y = v; }
+__device__ __forceinline__ void il_put(__nv_bfloat16* y, float v) { *y = __float2bfloat16_rn(v); }
+
+}  // namespace
+
+template <typename OutT>
+__global__ void __launch_bounds__(kIlThreads, 1)
+int8_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, const IlArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const int N = a.N, S = a.S;
+    const int stage_bytes = kIlABytes + N * 128;
+    IlShared& sh = *reinterpret_cast<IlShared*>(smem + (size_t)a.stages * stage_bytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = S > 1 ? (int)cluster_ctarank() : 0;
+    const int first = S > 1 ? (int)(blockIdx.x / S) : (int)blockIdx.x;
+    const int step = S > 1 ? (int)(gridDim.x / S) : (int)gridDim.x;
+    const int kb0 = (int)((long long)a.KB * rank / S), kb1 = (int)((long long)a.KB * (rank + 1) / S);
+    const int tiles = a.tiles_o * a.tiles_t;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < a.stages; ++i) {
+            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.acc_full[i], 1);
+            mbar_init(&sh.acc_empty[i], 8);
+        }
+        mbar_init(&sh.mma_done, 1);
+        fence_mbar_init();
+        sh.abort = 0;
+        prefetch_tmap(&tm_w);
+        prefetch_tmap(&tm_x);
+    }
+    if (warp == 2) {
+        tmem_alloc(&sh.tmem_base, 2 * N);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    griddep_launch_dependents();
+    const uint32_t tmem = sh.tmem_base;
+    const uint64_t limit = a.wait_ns;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint64_t pol = policy_evict_normal();
+            int st = 0;
+            uint32_t ph = 0;
+            bool stop = false;
+            // the first stages' weight tiles do not depend on the quantize kernel
+            int pre = 0;
+            if (first < tiles) {
+                const int to = first % a.tiles_o;
+                pre = min(a.stages, kb1 - kb0);
+                for (int i = 0; i < pre; ++i) {
+                    mbar_arrive_expect_tx(&sh.full[i], (uint32_t)stage_bytes);
+                    tma_load_2d(smem + (size_t)i * stage_bytes, &tm_w, &sh.full[i], (kb0 + i) * 128, to * 128, pol);
+                }
+            }
+            griddep_wait();
+            if (__ldcg(&a.ctl->status) != 0) sh.abort = 1;   // (the loads begun are still completed)
+            int issued = 0;
+            for (int tile = first; tile < tiles && !stop; tile += step) {
+                const int to = tile % a.tiles_o, tt = tile / a.tiles_o;
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    uint8_t* sp = smem + (size_t)st * stage_bytes;
+                    if (issued >= pre) {
+                        if (!wait_bar(&sh.empty[st], ph ^ 1u, limit, &sh.abort, a.ctl, kWaitEmpty)) {
+                            stop = true;
+                            break;
+                        }
+                        mbar_arrive_expect_tx(&sh.full[st], (uint32_t)stage_bytes);
+                        tma_load_2d(sp, &tm_w, &sh.full[st], kb * 128, to * 128, pol);
+                    }
+                    tma_load_2d(sp + kIlABytes, &tm_x, &sh.full[st], kb * 128, tt * N, pol);
+                    ++issued;
+                    if (++st == a.stages) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            // every load issued has landed before the block may end
+            const int in_ring = min(issued, a.stages);
+            for (int i = 0; i < in_ring; ++i) {
+                st = st == 0 ? a.stages - 1 : st - 1;
+                const int nth = (issued - 1 - i) / a.stages;   // how often the stage was filled before
+                wait_bar_drain(&sh.full[st], (uint32_t)(nth & 1), limit, a.ctl);
+            }
+        }
+    } else if (warp == 1) {
+        const uint32_t idesc = idesc_i8_s32(128, N);
+        const uint64_t desc0 = sw128_kmajor_desc(smem_u32(smem));
+        int st = 0, buf = 0;
+        uint32_t ph = 0, bph = 0;
+        bool ok = true;
+        for (int tile = first; tile < tiles && ok; tile += step) {
+            ok = wait_bar_warp(&sh.acc_empty[buf], bph ^ 1u, limit, &sh.abort, a.ctl, kWaitAccEmpty);
+            if (!ok) break;
+            tc_fence_after();
+            for (int kb = kb0; kb < kb1; ++kb) {
+                ok = wait_bar_warp(&sh.full[st], ph, limit, &sh.abort, a.ctl, kWaitFullW);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t ad = desc0 + (uint64_t)((uint32_t)st * (uint32_t)stage_bytes >> 4);
+                    const uint64_t bd = ad + (kIlABytes >> 4);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_i8(tmem + (uint32_t)(buf * N), ad + 2 * k, bd + 2 * k, idesc, kb > kb0 || k > 0);
+                    umma_commit(&sh.empty[st]);
+                    if (kb == kb1 - 1) umma_commit(&sh.acc_full[buf]);
+                }
+                __syncwarp();
+                if (++st == a.stages) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+            }
+            buf ^= 1;
+            if (buf == 0) bph ^= 1u;
+        }
+        // no MMA is in flight when the accumulators are given back
+        if (elect_one()) umma_commit(&sh.mma_done);
+        __syncwarp();
+        if (lane == 0) wait_bar_drain(&sh.mma_done, 0u, limit, a.ctl);
+        __syncwarp();
+    } else if (warp >= 4) {
+        griddep_wait();   // the token scales
+        const int q = warp & 3, half = (warp - 4) >> 2, ch = q * 32 + lane;
+        int buf = 0;
+        uint32_t bph = 0;
+        for (int tile = first; tile < tiles; tile += step) {
+            const int to = tile % a.tiles_o, tt = tile / a.tiles_o;
+            const int t0 = tt * N, o = to * 128 + ch;
+            // lanes 0-15 hold the scales of the columns of each of the group's pieces
+            float sx[8];
+#pragma unroll
+            for (int p = 0; p < 8; ++p) {
+                const int t = t0 + half * 16 + 32 * p + (lane & 15);
+                sx[p] = (half * 16 + 32 * p < N && t < a.T) ? __ldcg(a.sx + t) : 0.f;
+            }
+            const float sw = o < a.O ? __ldg(a.sw + o) : 0.f;
+            const float b = (a.bias != nullptr && o < a.O) ? __ldg(a.bias + o) : 0.f;
+            if (!wait_bar_warp(&sh.acc_full[buf], bph, limit, &sh.abort, a.ctl, kWaitAccFull)) break;
+            tc_fence_after();
+            const uint32_t tacc = tmem + (uint32_t)(buf * N) + ((uint32_t)(q * 32) << 16);
+            OutT* y = static_cast<OutT*>(a.y) + (size_t)t0 * a.O + o;
+            if (S == 1) {
+#pragma unroll
+                for (int p = 0; p < 8; ++p) {
+                    const int c = half * 16 + 32 * p;
+                    if (c < N) {
+                        uint32_t v[32];
+                        tmem_ld_32x32b_x16(tacc + (uint32_t)c, v);
+                        tmem_ld_wait();
+                        if (c + 32 >= N) {   // the group's last piece: its columns are in registers
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float st = __shfl_sync(0xffffffffu, sx[p], i);
+                            if (o < a.O && t0 + c + i < a.T)
+                                il_put(y + (size_t)(c + i) * a.O, fmaf((float)(int)v[i] * sw, st, b));
+                        }
+                    }
+                }
+                if (half * 16 >= N) {   // no piece of 16 columns for this group
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);
+                }
+            } else {
+                // this block's partial sums, [N][128] int32, over the stages (all read)
+                int* part = reinterpret_cast<int*>(smem);
+                for (int c = half * 16; c < N; c += 32) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x16(tacc + (uint32_t)c, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) part[(c + i) * 128 + ch] = (int)v[i];
+                }
+            }
+            buf ^= 1;
+            if (buf == 0) bph ^= 1u;
+        }
+    }
+    if (S > 1) {
+        // (every block of the cluster has the same tile: tiles == clusters)
+        cluster_barrier_sync();
+        if (warp >= 4 && first < tiles && sh.abort == 0) {
+            const int to = first % a.tiles_o, tt = first / a.tiles_o;
+            const int q = warp & 3, half = (warp - 4) >> 2, ch = q * 32 + lane;
+            const int t0 = tt * N, o = to * 128 + ch;
+            const float sw = o < a.O ? __ldg(a.sw + o) : 0.f;
+            const float b = (a.bias != nullptr && o < a.O) ? __ldg(a.bias + o) : 0.f;
+            OutT* y = static_cast<OutT*>(a.y) + (size_t)t0 * a.O + o;
+            const int c1 = min((N * (rank + 1)) / S, a.T - t0);
+            for (int c = (N * rank) / S + half; c < c1; c += 2) {
+                const uint32_t off = smem_u32(smem) + (uint32_t)(c * 128 + ch) * 4u;
+                int v = 0;
+                for (int r = 0; r < S; ++r) v += ld_shared_cluster_s32(mapa_shared(off, (uint32_t)r));
+                if (o < a.O) il_put(y + (size_t)c * a.O, fmaf((float)v * sw, a.sx[t0 + c], b));
+            }
+        }
+        cluster_barrier_sync();   // no block leaves while its partial sums may be read
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 2) tmem_dealloc(tmem, 2 * N);
+}
+
+namespace {
+size_t il_smem(int stages, int N) { return 1024 + (size_t)stages * (kIlABytes + N * 128) + sizeof(IlShared); }
+
+template <typename OutT>
+cudaError_t launch_il(const IlArgs& a, const CUtensorMap* maps, int grid, cudaStream_t s) {
+    const size_t smem = il_smem(a.stages, a.N);
+    auto kern = int8_linear_kernel<OutT>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(227 * 1024));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kIlThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)a.S;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = a.S > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], a);
+}
+}  // namespace
+
+// Tile width and K split.  A tile of N tokens costs about 2 N cycles of MMA for each
+// 128 bytes of K, or the time of its (128 + N) * 128 bytes at about 48 bytes per cycle
+// and SM, and some 1500 cycles of start and epilogue (more where a cluster meets);
+// the pair (N, S) with the smallest time over all waves is taken.
+void int8_linear_plan(int T, int K, int O, int sms, int* N_out, int* S_out) {
+    const int KB = (K + 127) / 128, tiles_o = (O + 127) / 128;
+    double best = 1e30;
+    *N_out = 256;
+    *S_out = 1;
+    for (int N = 16; N <= 256; N *= 2) {
+        const long long tiles = (long long)tiles_o * ((T + N - 1) / N);
+        for (int S = 1; S <= 8; S *= 2) {
+            // (clusters of S do not fill every SM: count them 8/9)
+            if (S > 1 && (N > 64 || tiles * S > (long long)sms * 8 / 9 || KB / S < 2)) continue;
+            const double waves = S > 1 ? 1.0 : (double)((tiles + sms - 1) / sms);
+            const double mma = 2.0 * N, load = (128.0 + N) * 128.0 / 48.0;
+            const double per = (double)((KB + S - 1) / S) * (mma > load ? mma : load);
+            const double cost = waves * (per + N * 4.0) + 1500.0 + (S > 1 ? 1200.0 : 0.0);
+            if (cost < best) {
+                best = cost;
+                *N_out = N;
+                *S_out = S;
+            }
+        }
+    }
+}
+
+cudaError_t launch_int8_linear(IlArgs a, const CUtensorMap* maps, bool bf16_out, int sms, cudaStream_t s) {
+    const int stage = kIlABytes + a.N * 128;
+    a.stages = kIlRing / stage < kIlMaxStages ? kIlRing / stage : kIlMaxStages;
+    const int tiles = a.tiles_o * a.tiles_t;
+    const int grid = a.S > 1 ? tiles * a.S : (tiles < sms ? tiles : sms);
+    return bf16_out ? launch_il<__nv_bfloat16>(a, maps, grid, s) : launch_il<float>(a, maps, grid, s);
+}
+
+}  // namespace bffn

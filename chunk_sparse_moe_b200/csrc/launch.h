@@ -120,4 +120,34 @@ size_t forward_decode_smem_bytes();
 // many blocks), -1 on error
 int decode_max_clusters();
 
+// top-k routing from logits and its gradient (route_topk.cu); bias and gates may be
+// nullptr
+cudaError_t launch_route_topk(const void* logits, bool bf16, const float* bias, int T, int E, int k, bool sigmoid,
+                              int n_group, int topk_group, bool renorm, float scale, float* gates, int32_t* ids,
+                              float* weights, cudaStream_t s);
+cudaError_t launch_route_topk_backward(const void* logits, bool bf16, const int32_t* ids, const float* d_weights, int T,
+                                       int E, int k, bool sigmoid, bool renorm, float scale, void* d_logits,
+                                       cudaStream_t s);
+
+// rows of K values rounded to 8 bits, one scale per row (int8_linear.cu)
+cudaError_t launch_quantize_rows(const void* v, bool bf16, int rows, int K, int8_t* q, float* scale, cudaStream_t s);
+
+// Arguments of the 8-bit integer product (int8_linear.cu).
+struct IlArgs {
+    const float* sx;          // [T] token scales
+    const float* sw;          // [O] channel scales
+    const float* bias;        // [O] or nullptr
+    void* y;                  // [T, O]
+    Ctl* ctl;
+    int T, O;
+    int KB;                   // 128-byte blocks of K
+    int N, S;                 // tokens per tile, blocks per tile (K split)
+    int tiles_o, tiles_t;
+    int stages;               // set by the launcher
+    unsigned long long wait_ns;
+};
+void int8_linear_plan(int T, int K, int O, int sms, int* N, int* S);
+// maps: W [O, K] (box {128, 128}) and q [T, K] (box {128, N}), bytes, 128-byte swizzle
+cudaError_t launch_int8_linear(IlArgs a, const CUtensorMap* maps, bool bf16_out, int sms, cudaStream_t s);
+
 }  // namespace bffn

@@ -131,6 +131,90 @@ blockffn_status blockffn_residual_layernorm(const void* y, const void* x, const 
                                            const float* ln_beta, float eps, int T, int d_h,
                                            blockffn_dtype dt, void* out, void* stream);
 
+/* Scores of the top-k router. */
+typedef enum {
+    BLOCKFFN_SOFTMAX = 0, /* s = softmax(logits) over the experts                      */
+    BLOCKFFN_SIGMOID = 1  /* s = 1 / (1 + exp(-logit)) for each expert                 */
+} blockffn_scores;
+
+/*
+ * blockffn_route_topk -- top-k routing from router logits.  No counterpart in the
+ * pages, whose router is blockffn_route: the usual alternative to it, with gates in
+ * the same form, so that blockffn_chunk_union and the forwards take them.
+ *
+ *   s      = scores of logits[t, :];  c[e] = s[e] + (bias ? bias[e] : 0)
+ *   groups : n_group groups of E / n_group neighbouring experts; a group's value is the
+ *            sum of its two largest c (of its one, where it has one); the topk_group
+ *            groups of largest value take part (all, when topk_group == n_group)
+ *   ids    = the k largest c among them, in descending order
+ *   w[i]   = s[ids[i]], divided by the sum of the chosen s when renormalize is set,
+ *            times scale.  The bias takes part in the choice only.
+ *   gates[t, :] = 0 except gates[t, ids[i]] = w[i]
+ *
+ * Ties go to the lowest expert (group) index; the choice is that of the exact
+ * scores, not of rounded ones.  logits [T, E] in dt.  An expert whose logit (or
+ * bias) is -infinity or NaN is never chosen; +infinity counts as the largest
+ * finite value.  A token with fewer than k choosable experts in its groups has
+ * ids -1 and weights 0 at the end of its list (a fully masked one: everywhere).
+ * A gate can be an exact zero where its score underflows; such an expert is
+ * listed in ids but not active for the forwards.
+ * Outputs: gates [T, E] fp32 or NULL, ids [T, k] int32, weights [T, k] fp32.
+ * Requirements: T >= 0, 1 <= E <= 256, n_group divides E, 1 <= topk_group <= n_group,
+ * 1 <= k <= min(32, topk_group * E / n_group), scale finite.
+ */
+blockffn_status blockffn_route_topk(const void* logits, blockffn_dtype dt, const float* bias, int T, int E,
+                                    int k, blockffn_scores scores, int n_group, int topk_group,
+                                    int renormalize, float scale, float* gates, int32_t* ids,
+                                    float* weights, void* stream);
+
+/*
+ * blockffn_route_topk_backward -- the gradient of blockffn_route_topk's weights with
+ * respect to the logits, the choice held fixed (the bias and the groups only choose,
+ * so they have no gradient):
+ *   d_logits[t, e] = sum_i d_weights[t, i] * d weights[t, i] / d logits[t, e]
+ * logits [T, E] in dt and ids [T, k] as given to and returned by blockffn_route_topk;
+ * d_weights [T, k] fp32 (where the gradient of the dense gates is at hand, its values
+ * at ids); scores, renormalize and scale as in the forward; d_logits [T, E] in dt,
+ * fully overwritten.  An id outside [0, E) has no gradient (its d_weights is not read
+ * into the result); an id listed twice counts twice.
+ */
+blockffn_status blockffn_route_topk_backward(const void* logits, blockffn_dtype dt, const int32_t* ids,
+                                             const float* d_weights, int T, int E, int k,
+                                             blockffn_scores scores, int renormalize, float scale,
+                                             void* d_logits, void* stream);
+
+/*
+ * blockffn_quantize_int8 -- rows in 8 bits with one scale each:
+ *   scale[r] = max_k |w[r,k]| / 127,   q[r,k] = round_to_even(127 w[r,k] / max_k |w[r,k]|)
+ * so w[r,k] is about q[r,k] scale[r] and q is in [-127, 127].  A row below 2^-120
+ * in magnitude has q = 0, scale = 0; a row holding an infinity or NaN has scale NaN
+ * and q = 0.  Lays out weights (a row is an output channel: scales per channel);
+ * the 8-bit products round their tokens the same way.
+ * w [rows, cols] in dt; q [rows, cols]; scale [rows] fp32.  cols <= 2^26.
+ */
+blockffn_status blockffn_quantize_int8(const void* w, int rows, int cols, blockffn_dtype dt, int8_t* q,
+                                       float* scale, void* stream);
+
+/*
+ * blockffn_int8_linear -- a linear layer in 8-bit integers, one scale for each token
+ * and each output channel:
+ *   (q_t, s_t) = blockffn_quantize_int8 of row x[t, :]
+ *   y[t,o]     = s_t s_w[o] sum_k q_t[k] W[o,k] + (bias ? bias[o] : 0)
+ * The integer sum is exact (int32); y is rounded once to y_dt.
+ * x [T, K] in dt; W [O, K] int8; s_w [O] fp32; bias [O] fp32 or NULL; y [T, O] in y_dt.
+ * A token with an infinity or NaN gives a row of NaN.
+ * workspace: ws_bytes >= blockffn_int8_linear_workspace_bytes(T, K, O) (0 for shapes
+ * that are refused), reset once before its first use; it holds nothing between
+ * calls but the status word, so calls of any shapes may share one that is large
+ * enough, as long as they cannot overlap on the GPU.  After a device-side error the
+ * outputs of that call are undefined.
+ * Requirements: T >= 0, O >= 1, K >= 16 a multiple of 16, K <= 131056.
+ */
+size_t blockffn_int8_linear_workspace_bytes(int T, int K, int O);
+blockffn_status blockffn_int8_linear(const void* x, blockffn_dtype dt, const int8_t* W, const float* s_w,
+                                     const float* bias, int T, int K, int O, blockffn_dtype y_dt, void* y,
+                                     void* workspace, size_t ws_bytes, void* stream);
+
 /*
  * blockffn_layer_opts -- the optional parts of the layer around the expert sum,
  * passed to blockffn_forward (a NULL pointer there means none of them).

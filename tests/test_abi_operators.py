@@ -1,0 +1,74 @@
+"""Host-side refusals of the top-k router and the 8-bit products: made before any CUDA
+call, so they run on a machine without a GPU."""
+import pytest
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from chunk_sparse_moe_b200 import build
+    build.build()
+    from chunk_sparse_moe_b200 import _lib
+    return _lib
+
+
+ROUTE = dict(logits=16, dt=0, bias=None, T=4, E=32, k=2, scores=0, n_group=1, topk_group=1, renorm=1, scale=1.0,
+             gates=16, ids=16, weights=16, stream=None)
+
+
+@pytest.mark.parametrize("change", [
+    dict(dt=2), dict(scores=2), dict(scores=-1), dict(T=-1), dict(E=0), dict(E=257), dict(k=0), dict(k=33),
+    dict(E=16, k=17), dict(n_group=0), dict(n_group=5), dict(n_group=4, topk_group=0), dict(n_group=4, topk_group=5),
+    dict(n_group=8, topk_group=1, k=5), dict(scale=float("inf")), dict(scale=float("nan")), dict(logits=None),
+    dict(ids=None), dict(weights=None), dict(logits=18), dict(ids=24), dict(weights=20), dict(bias=20), dict(gates=8)])
+def test_route_topk_refuses(lib, change):
+    assert lib.lib.blockffn_route_topk(*{**ROUTE, **change}.values()) == lib.ERR_INVALID_ARG
+    assert lib.lib.blockffn_last_error_message()
+
+
+BACK = dict(logits=16, dt=0, ids=16, d_weights=16, T=4, E=32, k=2, scores=0, renorm=1, scale=1.0, d_logits=16,
+            stream=None)
+
+
+@pytest.mark.parametrize("change", [
+    dict(dt=7), dict(scores=3), dict(T=-2), dict(E=0), dict(E=300), dict(k=0), dict(k=33), dict(E=4, k=5),
+    dict(scale=float("nan")), dict(logits=None), dict(ids=None), dict(d_weights=None), dict(d_logits=None),
+    dict(logits=17), dict(ids=20), dict(d_weights=24), dict(d_logits=28)])
+def test_route_topk_backward_refuses(lib, change):
+    assert lib.lib.blockffn_route_topk_backward(*{**BACK, **change}.values()) == lib.ERR_INVALID_ARG
+
+
+def test_quantize_refuses(lib):
+    f = lib.lib.blockffn_quantize_int8
+    for bad in ((16, 4, 0, 0, 16, 16), (16, -1, 8, 0, 16, 16), (16, 4, 8, 5, 16, 16), (16, 4, 1 << 27, 0, 16, 16),
+                (None, 4, 8, 0, 16, 16), (16, 4, 8, 0, None, 16), (16, 4, 8, 0, 16, None), (18, 4, 8, 0, 16, 16),
+                (16, 4, 8, 0, 17, 16), (16, 4, 8, 0, 16, 20)):
+        assert f(*bad, None) == lib.ERR_INVALID_ARG
+
+
+LINEAR = dict(x=16, dt=1, W=16, s_w=16, bias=None, T=4, K=64, O=32, y_dt=1, y=16, ws=256, ws_bytes=1 << 20, stream=None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(dt=2), 1), (dict(y_dt=-1), 1), (dict(T=-1), 1), (dict(K=0), 1), (dict(O=0), 1), (dict(K=72), 2),
+    (dict(K=131072), 2), (dict(T=2 ** 31 - 1, O=2 ** 31 - 1), 2), (dict(x=None), 1), (dict(W=None), 1),
+    (dict(s_w=None), 1), (dict(y=None), 1), (dict(ws=None), 1), (dict(x=18), 1), (dict(W=24), 1), (dict(s_w=20), 1),
+    (dict(bias=20), 1), (dict(y=8), 1), (dict(ws=264), 1), (dict(ws_bytes=300), 5)])
+def test_int8_linear_refuses(lib, change, status):
+    assert lib.lib.blockffn_int8_linear(*{**LINEAR, **change}.values()) == status
+    assert lib.lib.blockffn_last_error_message()
+
+
+def test_int8_linear_workspace_size(lib):
+    f = lib.lib.blockffn_int8_linear_workspace_bytes
+    assert f(4, 72, 32) == 0 and f(-1, 64, 32) == 0 and f(4, 64, 0) == 0
+    assert f(1000, 4096, 1) >= 1000 * 4096 + 1000 * 4 + 256
+
+
+def test_no_rows_are_no_ops(lib):
+    L = lib.lib
+    none = {k: None for k in ("logits", "gates", "ids", "weights")}
+    assert L.blockffn_route_topk(*{**ROUTE, **none, "T": 0}.values()) == lib.OK
+    none = {k: None for k in ("logits", "ids", "d_weights", "d_logits")}
+    assert L.blockffn_route_topk_backward(*{**BACK, **none, "T": 0}.values()) == lib.OK
+    assert L.blockffn_quantize_int8(None, 0, 8, 0, None, None, None) == lib.OK
+    assert L.blockffn_int8_linear(*{**LINEAR, "x": None, "y": None, "ws": None, "T": 0}.values()) == lib.OK
