@@ -6,11 +6,11 @@ CUDA stream to the C ABI (include/blockffn.h).  All arithmetic runs in the
 library's kernels; PyTorch only provides device memory and streams.
 """
 from .api import (BlockFFNError, Workspace, chunk_union, debug_set_trace, debug_skip_flag, device_status,
-                  forward, int8_linear,
+                  forward, forward_int8, int8_linear,
                   num_sms, quantize_int8, residual_layernorm, route, route_topk, route_topk_backward,
                   set_wait_limit_ns, version, workspace_bytes)
 
 __all__ = ["BlockFFNError", "Workspace", "chunk_union", "debug_set_trace", "debug_skip_flag", "residual_layernorm",
            "device_status",
-           "forward", "int8_linear", "num_sms", "quantize_int8", "route", "route_topk", "route_topk_backward",
+           "forward", "forward_int8", "int8_linear", "num_sms", "quantize_int8", "route", "route_topk", "route_topk_backward",
            "set_wait_limit_ns", "version", "workspace_bytes"]

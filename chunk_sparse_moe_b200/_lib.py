@@ -58,6 +58,10 @@ SIGNATURES = {
     "blockffn_int8_linear_workspace_bytes": (c_size_t, [c_int, c_int, c_int]),
     "blockffn_int8_linear": (c_int, [c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_int, c_int,
                                      c_int, c_int, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "blockffn_forward_int8_workspace_bytes": (c_size_t, [c_int, c_int, c_int, c_int]),
+    "blockffn_forward_int8": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                      c_int, c_int, c_int, c_int, c_int, c_void_p, c_void_p,
+                                      c_void_p, c_size_t, c_void_p]),
     "blockffn_get_device_status": (c_int, [c_void_p, c_void_p, c_int32_p]),
     "blockffn_forward_noalloc": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int,
                                          c_int, c_int, c_int, c_void_p, c_void_p]),

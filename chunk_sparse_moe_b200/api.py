@@ -143,6 +143,13 @@ class Workspace:
         return cls(nb, device)
 
     @classmethod
+    def for_forward_int8(cls, T: int, d_h: int, E: int, d_e: int, device=None) -> "Workspace":
+        nb = int(lib.blockffn_forward_int8_workspace_bytes(T, d_h, E, d_e))
+        if nb == 0:
+            raise BlockFFNError(_lib.ERR_INVALID_ARG, "blockffn_forward_int8_workspace_bytes")
+        return cls(nb, device)
+
+    @classmethod
     def for_shapes(cls, T, d_h, E, d_e, n, dtype, with_router, device=None,
                    with_bias: bool = False) -> "Workspace":
         nb = workspace_bytes(T, d_h, E, d_e, n, dtype, with_router, with_bias)
@@ -307,6 +314,47 @@ def int8_linear(x: torch.Tensor, W: torch.Tensor, s_w: torch.Tensor, bias: Optio
         workspace = Workspace.for_int8_linear(T, K, O, dev)
     _launch("blockffn_int8_linear", lib.blockffn_int8_linear, dev, _ptr(x), _dtype_code(x), _ptr(W), _ptr(s_w),
             _ptr(bias), T, K, O, _dtype_code(y), _ptr(y), _ptr(workspace.buf), workspace.nbytes)
+    return y
+
+
+def forward_int8(x: torch.Tensor, gates: torch.Tensor, W_in: torch.Tensor, s_in: torch.Tensor,
+                 W_out: torch.Tensor, s_out: torch.Tensor, y: Optional[torch.Tensor] = None,
+                 workspace: Optional[Workspace] = None, b_in: Optional[torch.Tensor] = None,
+                 b_out: Optional[torch.Tensor] = None, ln_weight: Optional[torch.Tensor] = None,
+                 ln_bias: Optional[torch.Tensor] = None, ln_eps: float = 1e-5) -> torch.Tensor:
+    """y [T, d_h] = sum of gate * expert(x) over each token's active experts (gate != 0) with
+    both expert products in 8-bit integers, then LayerNorm(y + x) when ``ln_weight`` is
+    given.
+
+    ``x`` [T, d_h] bf16 and Swish's result are rounded to 8 bits with a scale per token
+    (and expert); ``W_in`` [E, d_e, d_h] and ``W_out`` [E, d_h, d_e] int8 have the channel
+    scales ``s_in`` [E, d_e] and ``s_out`` [E, d_h] fp32 (``quantize_int8``).  ``gates``
+    [T, E] fp32, as ``route`` and ``route_topk`` return them.  The optional parts are those
+    of ``forward``."""
+    T, d_h = x.shape
+    E, d_e, _ = W_in.shape
+    dev = x.device
+    _want(gates, "gates", torch.float32, (T, E), dev)
+    _want(W_in, "W_in", torch.int8, (E, d_e, d_h), dev)
+    _want(s_in, "s_in", torch.float32, (E, d_e), dev)
+    _want(W_out, "W_out", torch.int8, (E, d_h, d_e), dev)
+    _want(s_out, "s_out", torch.float32, (E, d_h), dev)
+    opts = None
+    if b_in is not None or b_out is not None or ln_weight is not None:
+        for t, what, shape in ((b_in, "b_in", (E, d_e)), (b_out, "b_out", (E, d_h)), (ln_weight, "ln_weight", (d_h,)),
+                               (ln_bias, "ln_bias", (d_h,))):
+            if t is not None:
+                _want(t, what, torch.float32, shape, dev)
+        opts = ctypes.byref(_lib.LayerOpts(_ptr(b_in), _ptr(b_out), _ptr(ln_weight), _ptr(ln_bias), float(ln_eps)))
+    if y is None:
+        y = torch.empty((T, d_h), dtype=x.dtype, device=dev)
+    else:
+        _want(y, "y", x.dtype, (T, d_h), dev)
+    if workspace is None:
+        workspace = Workspace.for_forward_int8(T, d_h, E, d_e, dev)
+    _launch("blockffn_forward_int8", lib.blockffn_forward_int8, dev, _ptr(x), _ptr(gates), _ptr(W_in), _ptr(s_in),
+            _ptr(W_out), _ptr(s_out), T, d_h, E, d_e, _dtype_code(x), opts, _ptr(y), _ptr(workspace.buf),
+            workspace.nbytes)
     return y
 
 

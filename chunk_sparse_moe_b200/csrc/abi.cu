@@ -133,7 +133,7 @@ bool make_map_plain(CUtensorMap* m, const void* base, uint64_t inner, uint64_t o
 }
 
 // 2-D tensor of bytes [outer, inner], box {128, box_outer}, 128-byte swizzle
-// (inner a multiple of 16).
+// (inner a multiple of 16; box_outer 1 for gathered rows).
 bool make_map_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint32_t box_outer) {
     auto fn = encode_fn();
     if (fn == nullptr) return false;
@@ -469,6 +469,148 @@ blockffn_status blockffn_int8_linear(const void* x, blockffn_dtype dt, const int
     if (e != cudaSuccess) return cuda_fail(e, "quantize launch");
     e = launch_int8_linear(a, maps, y_dt == BLOCKFFN_BF16, G, s);
     return e == cudaSuccess ? BLOCKFFN_OK : cuda_fail(e, "int8_linear launch");
+}
+
+namespace {
+
+constexpr int kX8Slice = 8192;   // tokens per slice: bounds the scratch, tokens are independent
+
+blockffn_status check_forward_int8(int T, int d_h, int E, int d_e) {
+    if (T < 0 || d_h < 1 || d_e < 1 || E < 1 || E > 256)
+        return fail(BLOCKFFN_ERR_INVALID_ARG, "bad shape (T = %d, d_h = %d, E = %d, d_e = %d)", T, d_h, E, d_e);
+    if (d_h % 128 != 0 || d_h > 131072 - 128)
+        return fail(BLOCKFFN_ERR_UNSUPPORTED, "forward_int8 needs d_h %% 128 == 0, d_h < 131072 (d_h = %d)", d_h);
+    if (d_e % 128 != 0 || d_e > 512)
+        return fail(BLOCKFFN_ERR_UNSUPPORTED, "forward_int8 needs d_e in {128, 256, 384, 512} (d_e = %d)", d_e);
+    return BLOCKFFN_OK;
+}
+
+struct X8Layout {
+    size_t counts, tpos, sx, list, fpair, xq, hq, total;
+    int Tcap;
+};
+X8Layout x8_layout(int T, int d_h, int E, int d_e) {
+    X8Layout L;
+    L.Tcap = T < kX8Slice ? (T > 0 ? T : 1) : kX8Slice;
+    const size_t P = (size_t)E * L.Tcap;
+    size_t off = sizeof(Ctl);
+    auto take = [&](size_t bytes) {
+        const size_t o = off;
+        off = align_up(off + bytes, 256);
+        return o;
+    };
+    L.counts = take((size_t)E * 4);
+    L.tpos = take((size_t)E * ((L.Tcap + 31) / 32 + 1) * 4);
+    L.sx = take((size_t)L.Tcap * 4);
+    L.list = take(P * 4);
+    L.fpair = take(P * 8);
+    L.xq = take((size_t)L.Tcap * d_h);
+    L.hq = take(P * d_e);
+    L.total = off;
+    return L;
+}
+
+}  // namespace
+
+size_t blockffn_forward_int8_workspace_bytes(int T, int d_h, int E, int d_e) {
+    if (check_forward_int8(T, d_h, E, d_e) != BLOCKFFN_OK) return 0;
+    return x8_layout(T, d_h, E, d_e).total;
+}
+
+blockffn_status blockffn_forward_int8(const void* x, const float* gates, const int8_t* W_in, const float* s_in,
+                                      const int8_t* W_out, const float* s_out, int T, int d_h, int E, int d_e,
+                                      blockffn_dtype dt, const blockffn_layer_opts* opts, void* y, void* workspace,
+                                      size_t ws_bytes, void* stream) {
+    if (dt != BLOCKFFN_F32 && dt != BLOCKFFN_BF16) return fail(BLOCKFFN_ERR_INVALID_ARG, "unknown dtype %d", (int)dt);
+    blockffn_status st = check_forward_int8(T, d_h, E, d_e);
+    if (st != BLOCKFFN_OK) return st;
+    if (dt != BLOCKFFN_BF16) return fail(BLOCKFFN_ERR_UNSUPPORTED, "forward_int8 takes bf16 tokens");
+    if (T == 0) return BLOCKFFN_OK;
+    if (!x || !gates || !W_in || !s_in || !W_out || !s_out || !y || !workspace)
+        return fail(BLOCKFFN_ERR_INVALID_ARG, "null pointer");
+    const float* b_in = opts ? opts->b_in : nullptr;
+    const float* b_out = opts ? opts->b_out : nullptr;
+    const float* ln_w = opts ? opts->ln_weight : nullptr;
+    const float* ln_b = (opts && ln_w) ? opts->ln_bias : nullptr;
+    const float ln_eps = opts ? opts->ln_eps : 0.f;
+    if (ln_w && (!(ln_eps >= 0.f) || !std::isfinite(ln_eps)))
+        return fail(BLOCKFFN_ERR_INVALID_ARG, "ln_eps must be finite and >= 0");
+    if (!aligned16(x) || !aligned16(gates) || !aligned16(W_in) || !aligned16(s_in) || !aligned16(W_out) ||
+        !aligned16(s_out) || !aligned16(y) || !aligned16(workspace) || (b_in && !aligned16(b_in)) ||
+        (b_out && !aligned16(b_out)) || (ln_w && !aligned16(ln_w)) || (ln_b && !aligned16(ln_b)))
+        return fail(BLOCKFFN_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
+    const X8Layout L = x8_layout(T, d_h, E, d_e);
+    if (ws_bytes < L.total)
+        return fail(BLOCKFFN_ERR_WORKSPACE, "workspace of %zu bytes < %zu needed", ws_bytes, L.total);
+    const int G = num_sms_current();
+    if (G <= 0) return fail(BLOCKFFN_ERR_CUDA, "no current CUDA device");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    char* ws = static_cast<char*>(workspace);
+    X8Bufs w;
+    w.xq = reinterpret_cast<int8_t*>(ws + L.xq);
+    w.sx = reinterpret_cast<float*>(ws + L.sx);
+    w.counts = reinterpret_cast<int32_t*>(ws + L.counts);
+    w.list = reinterpret_cast<int32_t*>(ws + L.list);
+    w.tpos = reinterpret_cast<int32_t*>(ws + L.tpos);
+    w.fpair = reinterpret_cast<float2*>(ws + L.fpair);
+    w.hq = reinterpret_cast<int8_t*>(ws + L.hq);
+    w.Tcap = L.Tcap;
+    Ctl* ctl = reinterpret_cast<Ctl*>(ws);
+    const int MT = d_e / 128;
+    for (int t0 = 0; t0 < T; t0 += L.Tcap) {
+        const int n = T - t0 < L.Tcap ? T - t0 : L.Tcap;
+        const __nv_bfloat16* xs = static_cast<const __nv_bfloat16*>(x) + (size_t)t0 * d_h;
+        const float* gs = gates + (size_t)t0 * E;
+        w.C32 = (n + 31) / 32;
+        cudaError_t e = launch_int8_prepare(xs, gs, n, d_h, E, w, s);
+        if (e != cudaSuccess) return cuda_fail(e, "8-bit prepare launch");
+        X8In in;
+        in.w = w;
+        in.gates = gs;
+        in.s_in = s_in;
+        in.b_in = b_in;
+        in.ctl = ctl;
+        in.E = E;
+        in.d_e = d_e;
+        in.KB = d_h / 128;
+        in.N = n <= 16 ? 16 : n <= 32 ? 32 : (n <= 1024 || MT > 2) ? 64 : 128;
+        in.CS = n <= 128 ? 8 : n <= 1024 ? 2 : 1;
+        in.stages = 0;
+        in.wait_ns = g_wait_ns.load();
+        X8Out out;
+        out.w = w;
+        out.s_out = s_out;
+        out.b_out = b_out;
+        out.y = static_cast<__nv_bfloat16*>(y) + (size_t)t0 * d_h;
+        out.ctl = ctl;
+        out.T = n;
+        out.E = E;
+        out.d_h = d_h;
+        out.KBe = MT;
+        out.slabs = d_h / 128;
+        out.TT = n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256;
+        out.NB = n <= 16 ? 16 : n <= 32 ? 32 : 64;
+        out.S = 1;
+        const long long items = (long long)out.slabs * ((n + out.TT - 1) / out.TT);
+        while (out.S < 8 && items * out.S * 2 <= (long long)G * 8 / 9) out.S *= 2;
+        out.stages = 0;
+        out.wait_ns = in.wait_ns;
+        CUtensorMap maps[4];
+        if (!make_map_u8(&maps[0], W_in, (uint64_t)d_h, (uint64_t)E * d_e, 128) ||
+            !make_map_u8(&maps[1], w.xq, (uint64_t)d_h, (uint64_t)n, 1) ||
+            !make_map_u8(&maps[2], W_out, (uint64_t)d_e, (uint64_t)E * d_h, 128) ||
+            !make_map_u8(&maps[3], w.hq, (uint64_t)d_e, (uint64_t)E * L.Tcap, 16))
+            return fail(BLOCKFFN_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+        e = launch_int8_experts_in(in, maps, G, s);
+        if (e != cudaSuccess) return cuda_fail(e, "8-bit experts-in launch");
+        e = launch_int8_experts_out(out, maps + 2, s);
+        if (e != cudaSuccess) return cuda_fail(e, "8-bit experts-out launch");
+    }
+    if (ln_w) {
+        cudaError_t e = launch_residual_layernorm(y, x, ln_w, ln_b, ln_eps, T, d_h, true, y, s);
+        if (e != cudaSuccess) return cuda_fail(e, "residual layernorm launch");
+    }
+    return BLOCKFFN_OK;
 }
 
 size_t blockffn_forward_workspace_bytes(int T, int d_h, int E, int d_e, int n, blockffn_dtype dt, int flags) {

@@ -150,4 +150,53 @@ void int8_linear_plan(int T, int K, int O, int sms, int* N, int* S);
 // maps: W [O, K] (box {128, 128}) and q [T, K] (box {128, N}), bytes, 128-byte swizzle
 cudaError_t launch_int8_linear(IlArgs a, const CUtensorMap* maps, bool bf16_out, int sms, cudaStream_t s);
 
+// Scratch of the 8-bit expert sum (forward_int8.cu), for a slice of up to Tcap tokens.
+struct X8Bufs {
+    int8_t* xq;               // [Tcap, d_h] the tokens in 8 bits
+    float* sx;                // [Tcap] their scales
+    int32_t* counts;          // [E] tokens of each expert
+    int32_t* list;            // [E, Tcap] the tokens of each expert, ascending
+    int32_t* tpos;            // [E, C32 + 1] how many of them come before token 32 c (last: all)
+    float2* fpair;            // [E, Tcap] gate * scale of h, and gate, of each listed token
+    int8_t* hq;               // [E * Tcap, d_e] h of each listed token in 8 bits
+    int Tcap;
+    int C32;                  // ceil(T / 32) of the slice
+};
+cudaError_t launch_int8_prepare(const __nv_bfloat16* x, const float* gates, int T, int d_h, int E, const X8Bufs& w,
+                                cudaStream_t s);
+
+struct X8In {
+    X8Bufs w;
+    const float* gates;       // [T, E]
+    const float* s_in;        // [E, d_e]
+    const float* b_in;        // [E, d_e] or nullptr
+    Ctl* ctl;
+    int E, d_e;
+    int KB;                   // d_h / 128
+    int N;                    // tokens per tile
+    int CS;                   // blocks per cluster
+    int stages;               // set by the launcher
+    unsigned long long wait_ns;
+};
+// maps: W_in [E * d_e, d_h] (box {128, 128}) and xq [T, d_h] (box {128, 1}: gathered)
+cudaError_t launch_int8_experts_in(X8In a, const CUtensorMap* maps, int sms, cudaStream_t s);
+
+struct X8Out {
+    X8Bufs w;
+    const float* s_out;       // [E, d_h]
+    const float* b_out;       // [E, d_h] or nullptr
+    __nv_bfloat16* y;         // [T, d_h]
+    Ctl* ctl;
+    int T, E, d_h;
+    int KBe;                  // d_e / 128
+    int slabs;                // d_h / 128
+    int TT;                   // tokens per tile (a multiple of 32)
+    int NB;                   // pairs multiplied at a time (a multiple of 16, at most 64)
+    int S;                    // blocks per cluster
+    int stages;               // set by the launcher
+    unsigned long long wait_ns;
+};
+// maps: W_out [E * d_h, d_e] (box {128, 128}) and hq [E * Tcap, d_e] (box {128, 16})
+cudaError_t launch_int8_experts_out(X8Out a, const CUtensorMap* maps, cudaStream_t s);
+
 }  // namespace bffn

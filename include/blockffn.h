@@ -322,6 +322,38 @@ blockffn_status blockffn_forward(const void* x, const float* gates, const void* 
                                  void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * blockffn_forward_int8 -- the layer output with both expert products in 8-bit
+ * integers.  Pages: as blockffn_forward (the same sum); the 8-bit form is this
+ * library's.  For every token t and expert e with gates[t,e] != 0:
+ *   (xq, sx) = blockffn_quantize_int8 of row x[t, :]
+ *   z[j]     = sx s_in[e,j] sum_k xq[k] W_in[e,j,k] + (b_in ? b_in[e,j] : 0)
+ *   h        = Swish(z);  (hq, sh) = h rounded to 8 bits, one scale over the d_e values
+ *   y[t,o]  += gates[t,e] (sh s_out[e,o] sum_j hq[j] W_out[e,o,j] + (b_out ? b_out[e,o] : 0))
+ * then y <- LayerNorm(y + x) when opts->ln_weight is given.  The integer sums are exact
+ * (int32); the sum over experts is fp32 in a fixed order and is rounded once to dt.
+ * The chunk length plays no part: an expert is computed for the tokens that use it.
+ *
+ * x, y [T, d_h] bf16 (dt must be BLOCKFFN_BF16); gates [T, E] fp32; W_in [E, d_e, d_h]
+ * and W_out [E, d_h, d_e] int8 with channel scales s_in [E, d_e] and s_out [E, d_h]
+ * fp32; opts as in blockffn_forward.  y is fully overwritten (zeros for a token with no
+ * active expert, before a LayerNorm); a token that holds an infinity or NaN, or an
+ * active gate that is one, gives a row of NaN and touches no other row.
+ * workspace: ws_bytes >= blockffn_forward_int8_workspace_bytes(T, d_h, E, d_e) (0 for
+ * shapes that are refused), reset once before its first use; it holds nothing between
+ * calls but the status word, so calls of any shapes may share one that is large
+ * enough, as long as they cannot overlap on the GPU.  Inputs above 8192 tokens run in
+ * slices of that many.  After a device-side error the outputs of that call are
+ * undefined and later calls compute nothing until the workspace is reset.
+ * Requirements: T >= 0, 1 <= E <= 256, d_h % 128 == 0, d_e in {128, 256, 384, 512}.
+ */
+size_t blockffn_forward_int8_workspace_bytes(int T, int d_h, int E, int d_e);
+blockffn_status blockffn_forward_int8(const void* x, const float* gates, const int8_t* W_in,
+                                      const float* s_in, const int8_t* W_out, const float* s_out, int T,
+                                      int d_h, int E, int d_e, blockffn_dtype dt,
+                                      const blockffn_layer_opts* opts, void* y, void* workspace,
+                                      size_t ws_bytes, void* stream);
+
+/*
  * blockffn_forward_noalloc -- the same layer output as blockffn_forward for ONE
  * chunk with injected gates (T <= n, bf16), for callers that cannot allocate
  * device memory: code running where cudaMalloc is not allowed or not wanted,

@@ -72,3 +72,31 @@ def test_no_rows_are_no_ops(lib):
     assert L.blockffn_route_topk_backward(*{**BACK, **none, "T": 0}.values()) == lib.OK
     assert L.blockffn_quantize_int8(None, 0, 8, 0, None, None, None) == lib.OK
     assert L.blockffn_int8_linear(*{**LINEAR, "x": None, "y": None, "ws": None, "T": 0}.values()) == lib.OK
+
+
+FORWARD = dict(x=16, gates=16, W_in=16, s_in=16, W_out=16, s_out=16, T=4, d_h=256, E=8, d_e=128, dt=1, opts=None,
+               y=16, ws=256, ws_bytes=1 << 24, stream=None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(dt=5), 1), (dict(dt=0), 2), (dict(T=-1), 1), (dict(d_h=0), 1), (dict(d_h=200), 2), (dict(d_h=1 << 17), 2),
+    (dict(E=0), 1), (dict(E=257), 1), (dict(d_e=64), 2), (dict(d_e=640), 2), (dict(x=None), 1), (dict(gates=None), 1),
+    (dict(W_in=None), 1), (dict(s_in=None), 1), (dict(W_out=None), 1), (dict(s_out=None), 1), (dict(y=None), 1),
+    (dict(ws=None), 1), (dict(x=20), 1), (dict(gates=20), 1), (dict(W_in=24), 1), (dict(s_out=8), 1),
+    (dict(ws_bytes=1024), 5)])
+def test_forward_int8_refuses(lib, change, status):
+    assert lib.lib.blockffn_forward_int8(*{**FORWARD, **change}.values()) == status
+    assert lib.lib.blockffn_last_error_message()
+
+
+def test_forward_int8_options_and_sizes(lib):
+    import ctypes
+    L = lib.lib
+    for o in (lib.LayerOpts(20, None, None, None, 0.0), lib.LayerOpts(None, 24, None, None, 0.0),
+              lib.LayerOpts(None, None, 16, 20, 1e-5), lib.LayerOpts(None, None, 16, None, -1.0)):
+        assert L.blockffn_forward_int8(*{**FORWARD, "opts": ctypes.byref(o)}.values()) == lib.ERR_INVALID_ARG
+    f = L.blockffn_forward_int8_workspace_bytes
+    assert f(4, 200, 8, 128) == 0 and f(4, 256, 300, 128) == 0
+    # bounded by the slice: a long input needs no more than one of 8192 tokens
+    assert f(100000, 256, 8, 128) == f(8192, 256, 8, 128) > f(100, 256, 8, 128) > 0
+    assert L.blockffn_forward_int8(*{**FORWARD, "T": 0, "x": None, "y": None, "ws": None}.values()) == lib.OK

@@ -1,0 +1,244 @@
+"""GPU: the expert sum in 8-bit integers against the same formula in 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_common import require_cuda
+
+pytestmark = pytest.mark.gpu
+
+EPS = torch.finfo(torch.bfloat16).eps / 2
+
+
+def quantized(v):
+    amax = np.abs(v).max(-1, keepdims=True)
+    q = np.where(amax > 0, np.rint(v * 127 / np.where(amax > 0, amax, 1)), 0)
+    return q, amax[..., 0] / 127
+
+
+def reference(x, g, W_in, s_in, W_out, s_out, b_in=None, b_out=None):
+    """(y, how far fp32 steps and a rounding of h to the other side of a border may move it), fp64."""
+    T, d_h = x.shape
+    E = W_in.shape[0]
+    y, tol = np.zeros((T, d_h)), np.zeros((T, d_h))
+    xq, sx = quantized(x)
+    for e in range(E):
+        t = np.nonzero(g[:, e] != 0)[0]
+        if not len(t):
+            continue
+        z = (xq[t] @ W_in[e].T.astype(np.float64)) * sx[t, None] * s_in[e]
+        if b_in is not None:
+            z = z + b_in[e]
+        h = z / (1 + np.exp(-z))
+        hq, hs = quantized(h)
+        w = W_out[e].T.astype(np.float64)
+        o = (hq @ w) * hs[:, None] * s_out[e]
+        if b_out is not None:
+            o = o + b_out[e]
+        ge = g[t, e, None]
+        y[t] += ge * o
+        # values of h within 1e-4 of a step of the border between two whole numbers (fp32 z and Swish:
+        # some 2^-20 of |h|, at most 127 steps) may go to the other side: a step of hs each
+        near = np.abs(np.abs(h / np.where(hs[:, None] > 0, hs[:, None], 1) - hq) - 0.5) < 127 * 2.0 ** -20 * 4
+        flip = (near.astype(np.float64) @ np.abs(w)) * hs[:, None] * s_out[e]
+        tol[t] += np.abs(ge) * (flip + 2.0 ** -20 * (np.abs(hq) @ np.abs(w) * hs[:, None] * s_out[e] + np.abs(o)))
+    return y, tol
+
+
+def make(T, d_h, E, d_e, seed, active, biases=False):
+    """Inputs as numpy; ``active``: probability, or 'topk4', of a gate."""
+    rng = np.random.default_rng(seed)
+    x = torch.from_numpy(rng.standard_normal((T, d_h)).astype(np.float32)).to(torch.bfloat16)
+    W_in = rng.integers(-127, 128, (E, d_e, d_h)).astype(np.int8)
+    W_out = rng.integers(-127, 128, (E, d_h, d_e)).astype(np.int8)
+    s_in = ((0.5 + rng.random((E, d_e))) / 73 / np.sqrt(d_h)).astype(np.float32)
+    s_out = ((0.5 + rng.random((E, d_h))) / 73 / np.sqrt(d_e)).astype(np.float32)
+    if active == "topk4":
+        on = np.zeros((T, E), bool)
+        np.put_along_axis(on, rng.random((T, E)).argsort(1)[:, :4], True, 1)
+    else:
+        on = rng.random((T, E)) < active
+    g = np.where(on, rng.standard_normal((T, E)), 0).astype(np.float32)
+    b = (rng.standard_normal((E, d_e)).astype(np.float32) * 0.1,
+         rng.standard_normal((E, d_h)).astype(np.float32) * 0.1) if biases else (None, None)
+    return x, g, W_in, s_in, W_out, s_out, b[0], b[1]
+
+
+def call(bffn, d, **kw):
+    c = [None if a is None else (a if torch.is_tensor(a) else torch.from_numpy(a)).cuda() for a in d]
+    return bffn.forward_int8(*c[:6], b_in=c[6], b_out=c[7], **kw)
+
+
+def compare(y, d, rows=None):
+    want, tol = reference(d[0].double().numpy(), *[None if a is None else a.astype(np.float64) for a in d[1:]])
+    got = y.double().cpu().numpy()
+    if rows is not None:
+        want, tol, got = want[rows], tol[rows], got[rows]
+    assert np.all(np.abs(got - want) <= tol + 1.01 * EPS * (np.abs(want) + tol) + 1e-30)
+    none = ~np.any((d[1] if rows is None else d[1][rows]) != 0, axis=1)
+    if d[7] is None:
+        assert not got[none].any()
+
+
+CASES = [(1, 256, 16, 128, "topk4"), (1, 2048, 64, 128, "topk4"), (2, 128, 1, 128, 1.0), (7, 384, 5, 256, 0.5),
+         (16, 1024, 32, 512, 0.3), (32, 2048, 64, 128, 0.2), (32, 256, 256, 128, "topk4"), (33, 512, 8, 384, 0.5),
+         (50, 4096, 16, 128, "topk4"), (64, 512, 8, 512, 1.0), (100, 640, 24, 256, 0.1), (130, 256, 16, 128, 0.6),
+         (257, 512, 40, 128, "topk4"), (300, 256, 4, 512, 1.0), (1000, 256, 16, 384, 0.25), (1100, 384, 12, 128, 0.5),
+         (1500, 256, 6, 256, 0.9), (2051, 256, 32, 128, "topk4"), (600, 128, 200, 128, 0.02), (40, 1152, 16, 128, 0.0)]
+
+
+@pytest.mark.parametrize("T,d_h,E,d_e,active", CASES)
+def test_forward_int8(T, d_h, E, d_e, active):
+    bffn = require_cuda()
+    for biases in (False, True):
+        d = make(T, d_h, E, d_e, T + d_h + E, active, biases)
+        ws = bffn.Workspace.for_forward_int8(T, d_h, E, d_e)
+        y = call(bffn, d, workspace=ws)
+        assert bffn.device_status(ws) == (0, 0)
+        compare(y, d)
+
+
+def test_same_bits_shared_workspace_and_rows_behind():
+    """Two rounds of calls of different shapes through one workspace give the same bits; rows behind the
+    last token stay as they were."""
+    bffn = require_cuda()
+    shapes = CASES[:14]
+    ws = bffn.Workspace(max(bffn.Workspace.for_forward_int8(*s[:4]).nbytes for s in shapes))
+    first = []
+    for turn in range(2):
+        for n, s in enumerate(shapes):
+            d = make(*s[:4], n, s[4])
+            whole = torch.full((s[0] + 2, s[1]), 3.0, device="cuda", dtype=torch.bfloat16)
+            call(bffn, d, workspace=ws, y=whole[: s[0]])
+            assert torch.all(whole[s[0]:] == 3)
+            if turn == 0:
+                first.append(whole)
+            else:
+                assert torch.equal(whole, first[n])
+    assert bffn.device_status(ws) == (0, 0)
+
+
+def test_slices_of_a_long_input():
+    """More than 8192 tokens: slices through the same scratch, each row as if called alone."""
+    bffn = require_cuda()
+    T = 8192 + 77
+    d = make(T, 128, 4, 128, 1, 0.4)
+    y = call(bffn, d)
+    rows = np.r_[0:40, 8180:8192 + 77]
+    part = [d[0][rows], d[1][rows], *d[2:]]
+    compare(y[rows], part)
+    lone = call(bffn, [d[0][8192:], d[1][8192:], *d[2:]])
+    assert torch.equal(lone, y[8192:])
+
+
+def test_layernorm_and_in_place():
+    bffn = require_cuda()
+    T, d_h = 40, 512
+    d = make(T, d_h, 8, 128, 3, 0.5, True)
+    lw, lb = torch.rand(d_h).cuda(), torch.rand(d_h).cuda()
+    y = call(bffn, d)
+    want = bffn.residual_layernorm(y, d[0].cuda(), lw, lb)
+    assert torch.equal(call(bffn, d, ln_weight=lw, ln_bias=lb), want)
+    # y may be x itself without a LayerNorm: the tokens have been rounded before y is written
+    x = d[0].cuda()
+    c = [torch.from_numpy(a).cuda() for a in d[1:]]
+    bffn.forward_int8(x, *c[:5], b_in=c[5], b_out=c[6], y=x)
+    assert torch.equal(x, y)
+
+
+def test_infinite_tokens_and_gates_stay_in_their_rows():
+    bffn = require_cuda()
+    d = make(70, 256, 8, 128, 5, 0.5)
+    clean = call(bffn, d)
+    x, g = d[0].clone(), d[1].copy()
+    x[3, 5], x[40, 7] = float("inf"), float("nan")
+    g[3, 0] = g[40, 0] = 1.0
+    g[60, 2] = np.nan
+    y = call(bffn, [x, g, *d[2:]])
+    bad = [3, 40, 60]
+    assert torch.isnan(y[bad].float()).all()
+    rest = [t for t in range(70) if t not in bad]
+    assert torch.equal(y[rest], clean[rest])
+
+
+def test_stream_and_graph():
+    """On its own stream, and captured with the router before it and replayed on other tokens."""
+    bffn = require_cuda()
+    T, d_h, E, d_e = 32, 512, 32, 128
+    d = make(T, d_h, E, d_e, 6, 0.5)
+    c = [torch.from_numpy(a).cuda() for a in d[2:6]]
+    x = d[0].cuda()
+    z = torch.randn(T, E, device="cuda")
+    ws = bffn.Workspace.for_forward_int8(T, d_h, E, d_e)
+    out = bffn.route_topk(z, 4)
+    y = torch.empty_like(x)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        bffn.forward_int8(x, out[0], *c, y=y, workspace=ws)
+        with torch.cuda.graph(g, stream=side):
+            bffn.route_topk(z, 4, out=out)
+            bffn.forward_int8(x, out[0], *c, y=y, workspace=ws)
+    torch.cuda.synchronize()
+    for seed in (1, 2):
+        torch.manual_seed(seed)
+        z.normal_()
+        x.normal_()
+        g.replay()
+        torch.cuda.synchronize()
+        gates = bffn.route_topk(z, 4)[0]
+        assert torch.equal(y, bffn.forward_int8(x, gates, *c))
+    assert bffn.device_status(ws) == (0, 0)
+
+
+def test_layer_in_8_bits_end_to_end():
+    """The operators as a layer uses them: weights rounded once, logits from the 8-bit product, top-k
+    gates, 8-bit experts.  Near the same layer with unrounded weights: 8 bits are good for about 1 part in
+    100 of a random sum (a step is amax / 127, its error a third of that at most: relative
+    amax / (127 sqrt(12)) / rms per factor, 1 % with amax near 4 rms, and there are four)."""
+    bffn = require_cuda()
+    T, d_h, E, d_e, k = 96, 1024, 32, 128, 4
+    gen = torch.Generator().manual_seed(3)
+    r = lambda *s: torch.randn(*s, generator=gen)
+    x = r(T, d_h).bfloat16()
+    W_r, W_in, W_out = r(E, d_h) / d_h ** 0.5, r(E, d_e, d_h) / d_h ** 0.5, r(E, d_h, d_e) / d_e ** 0.5
+    (qr, sr), (qi, si), (qo, so) = (bffn.quantize_int8(w.cuda()) for w in (W_r, W_in, W_out))
+    logits = bffn.int8_linear(x.cuda(), qr, sr, out_dtype=torch.float32)
+    gates, ids, w = bffn.route_topk(logits, k)
+    y = bffn.forward_int8(x.cuda(), gates, qi, si, qo, so).double().cpu()
+    want_logits = x.double() @ W_r.double().T
+    assert torch.linalg.norm(logits.double().cpu() - want_logits) < 0.03 * torch.linalg.norm(want_logits)
+    want = torch.zeros(T, d_h, dtype=torch.float64)
+    g = gates.double().cpu()
+    for e in range(E):
+        z = x.double() @ W_in[e].double().T
+        want += g[:, e, None] * ((z * torch.sigmoid(z)) @ W_out[e].double().T)
+    assert torch.linalg.norm(y - want) < 0.05 * torch.linalg.norm(want)
+    # and the union form of the framework on the same gates and the weights that the 8 bits stand for
+    deq = [(q.float() * s[..., None]).bfloat16() for q, s in ((qi, si), (qo, so))]
+    y16 = bffn.forward(x.cuda(), *deq, 32, gates=gates).double().cpu()
+    assert torch.linalg.norm(y - y16) < 0.05 * torch.linalg.norm(y16)
+
+
+def test_empty_and_refusals():
+    bffn = require_cuda()
+    d = make(4, 256, 4, 128, 1, 0.5)
+    c = [d[0].cuda()] + [torch.from_numpy(a).cuda() for a in d[1:6]]
+    assert bffn.forward_int8(c[0][:0], c[1][:0], *c[2:]).shape == (0, 256)
+    with pytest.raises(bffn.BlockFFNError):
+        bffn.forward_int8(c[0].float(), *c[1:])
+    with pytest.raises(bffn.BlockFFNError):
+        bffn.forward_int8(*c, workspace=bffn.Workspace(256))
+    with pytest.raises(bffn.BlockFFNError):       # d_e 64
+        bffn.forward_int8(c[0], c[1], c[2][:, :64].contiguous(), c[3][:, :64].contiguous(),
+                          c[4][:, :, :64].contiguous(), c[5])
+    with pytest.raises(TypeError):
+        bffn.forward_int8(c[0], c[1].bfloat16(), *c[2:])
+    with pytest.raises(TypeError):
+        bffn.forward_int8(c[0], c[1], c[2].float(), *c[3:])
+    for i, bad in ((1, c[1][:3]), (3, c[3][:, :5]), (4, c[4][:3]), (5, c[5].t())):
+        with pytest.raises(ValueError):
+            bffn.forward_int8(*[bad if j == i else v for j, v in enumerate(c)])
+    with pytest.raises(ValueError):
+        bffn.forward_int8(*c, b_in=torch.zeros(4, 1, device="cuda"))
