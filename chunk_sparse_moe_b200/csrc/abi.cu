@@ -133,7 +133,7 @@ bool make_map_plain(CUtensorMap* m, const void* base, uint64_t inner, uint64_t o
 }
 
 // 2-D tensor of bytes [outer, inner], box {128, box_outer}, 128-byte swizzle
-// (inner a multiple of 16; box_outer 1 for gathered rows).
+// (inner a multiple of 16).
 bool make_map_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint32_t box_outer) {
     auto fn = encode_fn();
     if (fn == nullptr) return false;
@@ -486,7 +486,7 @@ blockffn_status check_forward_int8(int T, int d_h, int E, int d_e) {
 }
 
 struct X8Layout {
-    size_t counts, tpos, sx, list, fpair, xq, hq, total;
+    size_t counts, tpos, sx, list, pair, xq, hq, total;
     int Tcap;
 };
 X8Layout x8_layout(int T, int d_h, int E, int d_e) {
@@ -503,7 +503,7 @@ X8Layout x8_layout(int T, int d_h, int E, int d_e) {
     L.tpos = take((size_t)E * ((L.Tcap + 31) / 32 + 1) * 4);
     L.sx = take((size_t)L.Tcap * 4);
     L.list = take(P * 4);
-    L.fpair = take(P * 8);
+    L.pair = take(P * 16);
     L.xq = take((size_t)L.Tcap * d_h);
     L.hq = take(P * d_e);
     L.total = off;
@@ -552,7 +552,7 @@ blockffn_status blockffn_forward_int8(const void* x, const float* gates, const i
     w.counts = reinterpret_cast<int32_t*>(ws + L.counts);
     w.list = reinterpret_cast<int32_t*>(ws + L.list);
     w.tpos = reinterpret_cast<int32_t*>(ws + L.tpos);
-    w.fpair = reinterpret_cast<float2*>(ws + L.fpair);
+    w.pair = reinterpret_cast<float4*>(ws + L.pair);
     w.hq = reinterpret_cast<int8_t*>(ws + L.hq);
     w.Tcap = L.Tcap;
     Ctl* ctl = reinterpret_cast<Ctl*>(ws);
@@ -574,7 +574,7 @@ blockffn_status blockffn_forward_int8(const void* x, const float* gates, const i
         in.d_e = d_e;
         in.KB = d_h / 128;
         in.N = n <= 16 ? 16 : n <= 32 ? 32 : (n <= 1024 || MT > 2) ? 64 : 128;
-        in.CS = n <= 128 ? 8 : n <= 1024 ? 2 : 1;
+        in.CS = n <= 128 ? 4 : n <= 1024 ? 2 : 1;
         in.stages = 0;
         in.wait_ns = g_wait_ns.load();
         X8Out out;
@@ -592,18 +592,20 @@ blockffn_status blockffn_forward_int8(const void* x, const float* gates, const i
         out.NB = n <= 16 ? 16 : n <= 32 ? 32 : 64;
         out.S = 1;
         const long long items = (long long)out.slabs * ((n + out.TT - 1) / out.TT);
-        while (out.S < 8 && items * out.S * 2 <= (long long)G * 8 / 9) out.S *= 2;
+        for (int S = 2; S <= 8; ++S)
+            if (items <= int8_cluster_capacity(S) && S <= E) out.S = S;
         out.stages = 0;
         out.wait_ns = in.wait_ns;
-        CUtensorMap maps[4];
+        CUtensorMap maps[5];
         if (!make_map_u8(&maps[0], W_in, (uint64_t)d_h, (uint64_t)E * d_e, 128) ||
-            !make_map_u8(&maps[1], w.xq, (uint64_t)d_h, (uint64_t)n, 1) ||
-            !make_map_u8(&maps[2], W_out, (uint64_t)d_e, (uint64_t)E * d_h, 128) ||
-            !make_map_u8(&maps[3], w.hq, (uint64_t)d_e, (uint64_t)E * L.Tcap, 16))
+            !make_map_u8(&maps[1], W_out, (uint64_t)d_e, (uint64_t)E * d_h, 128) ||
+            !make_map_u8(&maps[2], w.hq, (uint64_t)d_e, (uint64_t)E * L.Tcap, 16) ||
+            !make_map_u8(&maps[3], w.hq, (uint64_t)d_e, (uint64_t)E * L.Tcap, 32) ||
+            !make_map_u8(&maps[4], w.hq, (uint64_t)d_e, (uint64_t)E * L.Tcap, 64))
             return fail(BLOCKFFN_ERR_CUDA, "cuTensorMapEncodeTiled failed");
-        e = launch_int8_experts_in(in, maps, G, s);
+        e = launch_int8_experts_in(in, maps[0], G, s);
         if (e != cudaSuccess) return cuda_fail(e, "8-bit experts-in launch");
-        e = launch_int8_experts_out(out, maps + 2, s);
+        e = launch_int8_experts_out(out, maps + 1, s);
         if (e != cudaSuccess) return cuda_fail(e, "8-bit experts-out launch");
     }
     if (ln_w) {

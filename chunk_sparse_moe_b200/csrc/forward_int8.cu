@@ -18,8 +18,9 @@
 //   prepare    : the tokens' 8-bit rows; per expert the ascending list of its tokens
 //                and, at every 32nd token, how many came before
 //   experts_in : tiles of one expert x up to N of its tokens, all of d_e; x rows are
-//                gathered by TMA (four rows an operation) straight into the MMA's
-//                layout.  The tile holds whole rows of h, so the epilogue finds
+//                gathered in 16-byte asynchronous copies straight into the MMA's
+//                swizzled layout (two warps; TMA's gather of four rows an operation took
+//                about 60 cycles each, 18 us for a tile of 128 rows at d_h 2048).  The tile holds whole rows of h, so the epilogue finds
 //                their scales and writes 8-bit h.  Few tiles: a cluster's blocks
 //                split d_h and add their int32 sums through distributed shared memory.
 //   experts_out: a block owns TT consecutive tokens x 128 output channels as fp32
@@ -40,50 +41,74 @@ namespace bffn {
 namespace {
 
 // ------------------------------------------------------------------ prepare --
-// Blocks 0 .. E-1 list an expert's tokens, block E + t rounds token t.
-constexpr int kPrepBatch = 8;   // gates a thread has in flight
+// Blocks 0 .. E-1 list an expert's tokens; the blocks behind them round tokens.
+constexpr int kPrepBatch = 16;   // gates a thread has in flight
 
-template <bool VEC>
-__global__ void __launch_bounds__(256) int8_prepare_kernel(const __nv_bfloat16* __restrict__ x,
-                                                           const float* __restrict__ gates, int T, int d_h, int E,
-                                                           const X8Bufs w) {
-    __shared__ uint32_t red[8];
+template <int C>
+__global__ void __launch_bounds__(kQThreads, 3) int8_prepare_kernel(const __nv_bfloat16* __restrict__ x,
+                                                                 const float* __restrict__ gates, int T, int d_h,
+                                                                 int E, int W, const X8Bufs w) {
+    constexpr int kWarps = kQThreads / 32;
+    __shared__ uint32_t red[kPrepBatch * kWarps + 1];
     griddep_wait();
     griddep_launch_dependents();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if ((int)blockIdx.x >= E) {
-        const int t = blockIdx.x - E;
-        quantize_row<__nv_bfloat16, VEC>(x + (size_t)t * d_h, d_h, w.xq + (size_t)t * d_h, w.sx + t, red);
+        const int g = tid / W, t = ((int)blockIdx.x - E) * (kQThreads / W) + g;
+        if (t < T)
+            quantize_row<__nv_bfloat16, C>(x + (size_t)t * d_h, d_h, w.xq + (size_t)t * d_h, w.sx + t, W, tid - g * W,
+                                           1 + g, red + g * (W / 32));
         return;
     }
-    const int e = blockIdx.x, nt = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nw = nt >> 5;
+    const int e = blockIdx.x;
     int32_t* list = w.list + (size_t)e * w.Tcap;
     int32_t* tpos = w.tpos + (size_t)e * (w.C32 + 1);
     int base = 0;   // tokens listed so far
-    for (int b0 = 0; b0 < T; b0 += nt * kPrepBatch) {
-        float g[kPrepBatch];
+    for (int b0 = 0; b0 < T; b0 += kQThreads * kPrepBatch) {
+        uint32_t on[kPrepBatch];
 #pragma unroll
         for (int i = 0; i < kPrepBatch; ++i) {
-            const int t = b0 + i * nt + tid;
-            g[i] = t < T ? __ldcg(gates + (size_t)t * E + e) : 0.f;
+            const int t = b0 + i * kQThreads + tid;
+            on[i] = t < T ? __float_as_uint(__ldcg(gates + (size_t)t * E + e)) : 0u;
         }
 #pragma unroll
         for (int i = 0; i < kPrepBatch; ++i) {
-            const int t = b0 + i * nt + tid;
-            if (b0 + i * nt >= T) break;
-            const uint32_t on = __ballot_sync(0xffffffffu, g[i] != 0.f);
-            if (lane == 0) red[warp] = (uint32_t)__popc(on);
-            __syncthreads();
-            int before = base, all = 0;
-            for (int q = 0; q < nw; ++q) {
-                const int c = (int)red[q];
-                before += q < warp ? c : 0;
-                all += c;
+            on[i] = __ballot_sync(0xffffffffu, __uint_as_float(on[i]) != 0.f);
+            if (lane == 0) red[i * kWarps + warp] = (uint32_t)__popc(on[i]);
+        }
+        __syncthreads();
+        if (warp == 0) {   // running sums over the batch's warps, in token order
+            constexpr int kPer = kPrepBatch * kWarps / 32;
+            uint32_t c[kPer], s = 0;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                c[i] = red[kPer * lane + i];
+                s += c[i];
             }
-            if (lane == 0 && t < T) tpos[t >> 5] = before;
-            if (g[i] != 0.f) list[before + __popc(on & ((1u << lane) - 1u))] = t;
-            base += all;
-            __syncthreads();
+            const uint32_t mine = s;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t u = __shfl_up_sync(0xffffffffu, s, o);
+                s += lane >= o ? u : 0u;
+            }
+            uint32_t run = s - mine;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                red[kPer * lane + i] = run;
+                run += c[i];
+            }
+            if (lane == 31) red[kPrepBatch * kWarps] = s;
         }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kPrepBatch; ++i) {
+            const int t = b0 + i * kQThreads + tid;
+            const int before = base + (int)red[i * kWarps + warp];
+            if (lane == 0 && t < T) tpos[t >> 5] = before;
+            if (on[i] >> lane & 1u) list[before + __popc(on[i] & ((1u << lane) - 1u))] = t;
+        }
+        base += (int)red[kPrepBatch * kWarps];
+        __syncthreads();
     }
     if (tid == 0) {
         tpos[w.C32] = base;
@@ -92,13 +117,17 @@ __global__ void __launch_bounds__(256) int8_prepare_kernel(const __nv_bfloat16* 
 }
 
 // --------------------------------------------------------------- experts_in --
-constexpr int kXThreads = 384;
+constexpr int kXGather = 4;                  // gathering warps of experts_in: 2, 3, 12, ..
+constexpr int kXiThreads = 384 + 32 * (kXGather - 2);
+constexpr int kXStep = 4 * kXGather;         // token rows they copy at a time
+constexpr int kXRows = 128 / kXStep;
 constexpr int kXMaxStages = 10;
 constexpr int kXTile = 128 * 128;            // 128 rows x 128 int8
 constexpr int kXRing = 200 * 1024;
 
 struct XiShared {
-    uint64_t full[kXMaxStages];
+    uint64_t full[kXMaxStages];              // weight tiles landed (bytes)
+    uint64_t gathered[kXMaxStages];          // token rows copied (the gathering warps)
     uint64_t empty[kXMaxStages];
     uint64_t acc_full[2];
     uint64_t acc_empty[2];
@@ -107,6 +136,7 @@ struct XiShared {
     volatile int abort;
     uint32_t colmax[2][2][4][16];            // by warp group, piece parity, warp
     int cnt[256];
+    int per[256];                            // tokens of each of an expert's tiles
     int first[257];                          // first tile of each expert
 };
 
@@ -114,20 +144,19 @@ struct XiItem {
     int e, base, rows;
 };
 // Tile i: expert e, tokens base .. base + rows of its list.  An expert's tokens are dealt
-// evenly to its tiles, in sixteens.
-__device__ __forceinline__ XiItem xi_item(const XiShared& sh, int E, int N, int i) {
-    int lo = 0, hi = E;
-    while (hi - lo > 1) {
-        const int m = (lo + hi) >> 1;
-        if (sh.first[m] <= i) lo = m;
-        else hi = m;
+// evenly to its tiles, in sixteens.  Called by whole warps.
+__device__ __forceinline__ XiItem xi_item(const XiShared& sh, int E, int i) {
+    const int lane = threadIdx.x & 31;
+    int e = -1;   // the last expert whose first tile is not behind i
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if (32 * j >= E) break;
+        e += __popc(__ballot_sync(0xffffffffu, 32 * j + lane < E && sh.first[32 * j + lane] <= i));
     }
     XiItem it;
-    it.e = lo;
-    const int cnt = sh.cnt[lo], nt = (cnt + N - 1) / N;
-    const int per = ((cnt + nt - 1) / nt + 15) & ~15;
-    it.base = (i - sh.first[lo]) * per;
-    it.rows = min(per, cnt - it.base);
+    it.e = e;
+    it.base = (i - sh.first[e]) * sh.per[e];
+    it.rows = min(sh.per[e], sh.cnt[e] - it.base);
     return it;
 }
 
@@ -145,17 +174,24 @@ __device__ __forceinline__ bool bar_all(int id, bool v) {
     return r != 0;
 }
 
-// What the epilogue does with n <= 16 columns (tokens) of int32 sums: h, its scale over
+__device__ __forceinline__ void tmem_ld_piece(uint32_t taddr, int (&v)[8]) {
+    uint32_t u[8];
+    tmem_ld_32x32b_x8(taddr, u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = (int)u[j];
+}
+
+// What the epilogue does with n <= PW columns (tokens) of int32 sums: h, its scale over
 // all of d_e (the four warps of the group meet in colmax), 8-bit h and the pair's factors.
-// Lane i (of 16) holds column i's token scale and gate.
-template <int MT>
-__device__ __forceinline__ void xi_finish(const X8In& a, XiShared& sh, const int (&v)[MT][16], int n, int e,
-                                          size_t pair0, float sx, float gate, const float (&si)[MT],
+// Lane i (of PW) holds column i's token, its scale and gate.
+template <int MT, int PW>
+__device__ __forceinline__ void xi_finish(const X8In& a, XiShared& sh, const int (&v)[MT][PW], int n,
+                                          size_t pair0, int token, float sx, float gate, const float (&si)[MT],
                                           const float (&bi)[MT], int group, int q, int lane, uint32_t& parity) {
-    float h[MT][16];
+    float h[MT][PW];
     uint32_t mine = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < PW; ++i) {
         const float s = __shfl_sync(0xffffffffu, sx, i);
         uint32_t m = 0;
 #pragma unroll
@@ -169,14 +205,15 @@ __device__ __forceinline__ void xi_finish(const X8In& a, XiShared& sh, const int
     }
     uint32_t (&cm)[4][16] = sh.colmax[group][parity];
     parity ^= 1u;   // (the other buffer next: this one is read until the next barrier)
-    if (lane < 16) cm[q][lane] = mine;
+    if (lane < PW) cm[q][lane] = mine;
     named_bar_sync(1 + group, 128);
     RowScale r = {0.f, 0.f, 0.f};
-    if (lane < 16) r = row_scale(max(max(cm[0][lane], cm[1][lane]), max(cm[2][lane], cm[3][lane])));
-    if (q == 0 && lane < n) a.w.fpair[pair0 + lane] = make_float2(gate * r.scale, gate);
+    if (lane < PW) r = row_scale(max(max(cm[0][lane], cm[1][lane]), max(cm[2][lane], cm[3][lane])));
+    if (q == 0 && lane < n)
+        a.w.pair[pair0 + lane] = make_float4(__int_as_float(token), gate * r.scale, gate, 0.f);
     int8_t* out = a.w.hq + pair0 * a.d_e + q * 32 + lane;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < PW; ++i) {
         const float inv = __shfl_sync(0xffffffffu, r.inv, i);
         if (i < n) {
 #pragma unroll
@@ -188,11 +225,13 @@ __device__ __forceinline__ void xi_finish(const X8In& a, XiShared& sh, const int
 }  // namespace
 
 template <int MT>
-__global__ void __launch_bounds__(kXThreads, 1)
-int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
-                       const X8In a) {
+__global__ void __launch_bounds__(kXiThreads, 1)
+int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const X8In a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    // Columns the epilogue holds at a time.  (Small pieces in rolled loops: at a decode step every
+    // instruction of the epilogue runs once, from a cold instruction cache.)
+    constexpr int PW = 8, PWX = 4;
     const int N = a.N;
     const int a_bytes = MT * kXTile, stage_bytes = a_bytes + N * 128;
     XiShared& sh = *reinterpret_cast<XiShared*>(smem + (size_t)a.stages * stage_bytes);
@@ -205,6 +244,7 @@ int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_co
     if (threadIdx.x == 0) {
         for (int i = 0; i < a.stages; ++i) {
             mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.gathered[i], kXGather);
             mbar_init(&sh.empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -215,21 +255,24 @@ int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_co
         fence_mbar_init();
         sh.abort = 0;
         prefetch_tmap(&tm_w);
-        prefetch_tmap(&tm_x);
     }
-    if (warp == 2) {
+    if (warp == 1) {
         tmem_alloc(&sh.tmem_base, cols);
         tmem_relinquish();
     }
     griddep_wait();
     griddep_launch_dependents();
-    if (warp == 3) {
+    if (warp == 0) {
         // tiles of each expert and their running count
+        const int status = __ldcg(&a.ctl->status);
+        int cnt[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) cnt[i] = 32 * i + lane < a.E ? __ldcg(a.w.counts + 32 * i + lane) : 0;
         int run = 0;
-        for (int e0 = 0; e0 < a.E; e0 += 32) {
-            const int e = e0 + lane;
-            const int cnt = e < a.E ? __ldcg(a.w.counts + e) : 0;
-            const int nt = (cnt + N - 1) / N;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (32 * i >= a.E) break;
+            const int e = 32 * i + lane, nt = (cnt[i] + N - 1) / N;
             int inc = nt;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -237,14 +280,15 @@ int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_co
                 inc += lane >= o ? u : 0;
             }
             if (e < a.E) {
-                sh.cnt[e] = cnt;
+                sh.cnt[e] = cnt[i];
+                sh.per[e] = nt > 0 ? ((cnt[i] + nt - 1) / nt + 15) & ~15 : 0;
                 sh.first[e] = run + inc - nt;
             }
             run += __shfl_sync(0xffffffffu, inc, 31);
         }
         if (lane == 0) {
             sh.first[a.E] = run;
-            if (__ldcg(&a.ctl->status) != 0) sh.abort = 1;
+            if (status != 0) sh.abort = 1;
         }
     }
     tc_fence_before();
@@ -264,32 +308,21 @@ int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_co
 
     if (warp == 0) {
         const uint64_t pol = policy_evict_normal();
-        int st = 0;
+        int st = 0, issued = 0;
         uint32_t ph = 0;
-        int issued = 0;
         bool ok = true;
         for (int i = first; i < tiles && ok; i += step) {
-            const XiItem it = xi_item(sh, a.E, N, i);
-            // lane l gathers rows 4 l .. 4 l + 3 (behind the last: the first again)
-            const int32_t* list = a.w.list + (size_t)it.e * a.w.Tcap + it.base;
-            const int quads = (it.rows + 3) >> 2;
-            int r[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) r[u] = __ldcg(list + (4 * lane + u < it.rows ? 4 * lane + u : 0));
-            const uint32_t bytes = (uint32_t)(a_bytes + quads * 512);
+            const XiItem it = xi_item(sh, a.E, i);
             for (int kb = kb0; kb < kb1; ++kb) {
                 ok = wait_bar_warp(&sh.empty[st], ph ^ 1u, limit, &sh.abort, a.ctl, kWaitEmpty);
                 if (!ok) break;
-                uint8_t* sp = smem + (size_t)st * stage_bytes;
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&sh.full[st], bytes);
+                    mbar_arrive_expect_tx(&sh.full[st], (uint32_t)a_bytes);
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
-                        tma_load_2d(sp + mt * kXTile, &tm_w, &sh.full[st], kb * 128, it.e * a.d_e + mt * 128, pol);
+                        tma_load_2d(smem + (size_t)st * stage_bytes + mt * kXTile, &tm_w, &sh.full[st], kb * 128,
+                                    it.e * a.d_e + mt * 128, pol);
                 }
-                __syncwarp();
-                if (lane < quads)
-                    tma_gather4(sp + a_bytes + lane * 512, &tm_x, &sh.full[st], kb * 128, r[0], r[1], r[2], r[3], pol);
                 __syncwarp();
                 ++issued;
                 if (++st == a.stages) {
@@ -307,21 +340,84 @@ int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_co
             }
         }
         __syncwarp();
+    } else if (warp == 2 || warp == 3 || warp >= 12) {
+        // Gather: eight lanes copy one token row's 128 bytes in 16-byte pieces into the
+        // swizzled layout (piece c of row r lies at c ^ (r & 7)); the warps take four rows
+        // each in turn.  The MMA reads the rows through the async proxy, and the fence
+        // that this takes waits for the block's copies in flight, so it is made once for
+        // half a ring of stages.
+        const int gw = warp < 4 ? warp - 2 : warp - 10;
+        const int r0 = gw * 4 + (lane >> 3), c = lane & 7;
+        const uint32_t dst0 = (uint32_t)(r0 * 128 + ((c ^ (r0 & 7)) << 4));
+        const int batch = a.stages / 2;
+        int st = 0, ann = 0, pending = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        int next[kXRows];   // the next tile's tokens, on their way
+        XiItem it = {0, 0, 0};
+        auto fetch = [&](int i) {
+            if (i >= tiles) return;
+            it = xi_item(sh, a.E, i);
+            const int32_t* list = a.w.list + (size_t)it.e * a.w.Tcap + it.base;
+#pragma unroll
+            for (int u = 0; u < kXRows; ++u) {
+                next[u] = 0;
+                if (kXStep * u < it.rows) next[u] = __ldcg(list + min(kXStep * u + r0, it.rows - 1));
+            }
+        };
+        fetch(first);
+        for (int i = first; i < tiles && ok; i += step) {
+            uint32_t tok[kXRows];
+            const int rows = it.rows;
+#pragma unroll
+            for (int u = 0; u < kXRows; ++u) tok[u] = (uint32_t)next[u] * (uint32_t)a.KB;   // in 128-byte rows
+            fetch(i + step);
+            for (int kb = kb0; kb < kb1; ++kb) {
+                ok = wait_bar_warp(&sh.empty[st], ph ^ 1u, limit, &sh.abort, a.ctl, kWaitEmpty);
+                if (!ok) break;
+                uint8_t* sp = smem + (size_t)st * stage_bytes + a_bytes + dst0;
+                const int8_t* src = a.w.xq + kb * 128 + c * 16;
+#pragma unroll
+                for (int u = 0; u < kXRows; ++u)
+                    if (kXStep * u < rows) cp_async_16(sp + u * kXStep * 128, src + (size_t)tok[u] * 128);
+                ++pending;
+                if (++st == a.stages) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+                if (pending >= batch || (kb == kb1 - 1 && i + step >= tiles)) {
+                    cp_async_wait_all();
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    for (; pending > 0; --pending) {
+                        if (lane == 0) mbar_arrive(&sh.gathered[ann]);
+                        if (++ann == a.stages) ann = 0;
+                    }
+                }
+            }
+        }
+        cp_async_wait_all();   // (after a timeout: no copy is in flight when the block ends)
+        __syncwarp();
     } else if (warp == 1) {
         const uint64_t desc0 = sw128_kmajor_desc(smem_u32(smem));
         int st = 0, buf = 0;
-        uint32_t ph = 0, bph = 0;
+        uint32_t ph = 0, bph = 0, got_w = 0, got_x = 0;   // (got: the next stage's barriers, tested ahead)
         bool ok = true;
         for (int i = first; i < tiles && ok; i += step) {
-            const XiItem it = xi_item(sh, a.E, N, i);
+            const XiItem it = xi_item(sh, a.E, i);
             const uint32_t idesc = idesc_i8_s32(128, (it.rows + 15) & ~15);
             ok = wait_bar_warp(&sh.acc_empty[buf], bph ^ 1u, limit, &sh.abort, a.ctl, kWaitAccEmpty);
             if (!ok) break;
             tc_fence_after();
             for (int kb = kb0; kb < kb1; ++kb) {
-                ok = wait_bar_warp(&sh.full[st], ph, limit, &sh.abort, a.ctl, kWaitFullW);
+                ok = wait_tested(got_w, &sh.full[st], ph, limit, &sh.abort, a.ctl, kWaitFullW) &&
+                     wait_tested(got_x, &sh.gathered[st], ph, limit, &sh.abort, a.ctl, kWaitFullW);
                 if (!ok) break;
                 tc_fence_after();
+                const int nst = st + 1 == a.stages ? 0 : st + 1;
+                const uint32_t nph = nst == 0 ? ph ^ 1u : ph;
+                got_w = mbar_test_wait(&sh.full[nst], nph);
+                got_x = mbar_test_wait(&sh.gathered[nst], nph);
                 if (elect_one()) {
                     const uint64_t ad = desc0 + (uint64_t)((uint32_t)st * (uint32_t)stage_bytes >> 4);
                     const uint64_t bd = ad + (uint64_t)(a_bytes >> 4);
@@ -335,10 +431,8 @@ int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_co
                     if (kb == kb1 - 1) umma_commit(&sh.acc_full[buf]);
                 }
                 __syncwarp();
-                if (++st == a.stages) {
-                    st = 0;
-                    ph ^= 1u;
-                }
+                st = nst;
+                ph = nph;
             }
             buf ^= 1;
             if (buf == 0) bph ^= 1u;
@@ -348,12 +442,12 @@ int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_co
         __syncwarp();
         if (lane == 0) wait_bar_drain(&sh.mma_done, 0u, limit, a.ctl);
         __syncwarp();
-    } else if (warp >= 4) {
+    } else {   // warps 4 .. 11
         const int q = warp & 3, group = (warp - 4) >> 2, ch = q * 32 + lane;
         int buf = 0;
         uint32_t bph = 0, parity = 0;
         for (int i = first; i < tiles; i += step) {
-            const XiItem it = xi_item(sh, a.E, N, i);
+            const XiItem it = xi_item(sh, a.E, i);
             const size_t pair = (size_t)it.e * a.w.Tcap + it.base;
             float si[MT], bi[MT];
 #pragma unroll
@@ -361,107 +455,117 @@ int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_co
                 si[mt] = __ldg(a.s_in + (size_t)it.e * a.d_e + mt * 128 + ch);
                 bi[mt] = a.b_in != nullptr ? __ldg(a.b_in + (size_t)it.e * a.d_e + mt * 128 + ch) : 0.f;
             }
-            float sx[4], gt[4];
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                const int c = group * 16 + 32 * p + (lane & 15);
-                sx[p] = gt[p] = 0.f;
-                if (S == 1 && c < it.rows) {
-                    const int t = __ldcg(a.w.list + pair + c);
-                    sx[p] = __ldcg(a.w.sx + t);
-                    gt[p] = __ldg(a.gates + (size_t)t * a.E + it.e);
-                }
-            }
             // (the group leaves its loop together)
             if (!bar_all(1 + group, wait_bar_warp(&sh.acc_full[buf], bph, limit, &sh.abort, a.ctl, kWaitAccFull))) break;
             tc_fence_after();
             const uint32_t tacc = tmem + (uint32_t)(buf * MT * N) + ((uint32_t)(q * 32) << 16);
             if (S == 1) {
-                if (group * 16 >= it.rows && lane == 0) mbar_arrive(&sh.acc_empty[buf]);   // nothing for this group
+                if (group * PW >= it.rows && lane == 0) mbar_arrive(&sh.acc_empty[buf]);   // nothing for this group
+                int tk = 0;
+                float sx = 0.f, gt = 0.f;
+                auto column = [&](int c) {   // what lane i (of PW) knows of column c + i
+                    c += lane & (PW - 1);
+                    if (c >= it.rows) return;
+                    tk = __ldcg(a.w.list + pair + c);
+                    sx = __ldcg(a.w.sx + tk);
+                    gt = __ldg(a.gates + (size_t)tk * a.E + it.e);
+                };
+                column(group * PW);
+#pragma unroll 1
+                for (int c = group * PW; c < it.rows; c += 2 * PW) {
+                    int v[MT][PW];
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    const int c = group * 16 + 32 * p;
-                    if (c < it.rows) {
-                        int v[MT][16];
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            uint32_t u[32];
-                            tmem_ld_32x32b_x16(tacc + (uint32_t)(mt * N + c), u);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) v[mt][j] = (int)u[j];
-                        }
-                        if (c + 32 >= it.rows) {   // the group's last piece is in registers
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);
-                        }
-                        xi_finish<MT>(a, sh, v, min(16, it.rows - c), it.e, pair + c, sx[p], gt[p], si, bi, group, q,
-                                      lane, parity);
+                    for (int mt = 0; mt < MT; ++mt) tmem_ld_piece(tacc + (uint32_t)(mt * N + c), v[mt]);
+                    const int tk0 = tk;
+                    const float sx0 = sx, gt0 = gt;
+                    column(c + 2 * PW);
+                    tmem_ld_wait();
+                    if (c + 2 * PW >= it.rows) {   // the group's last piece is in registers
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);
                     }
+                    xi_finish<MT, PW>(a, sh, v, min(PW, it.rows - c), pair + c, tk0, sx0, gt0, si, bi, group, q, lane,
+                                      parity);
                 }
             } else {
                 // partial sums [column][MT * 128] int32 over the stages (all read)
                 int* part = reinterpret_cast<int*>(smem);
-                for (int c = group * 16; c < it.rows; c += 32)
+#pragma unroll 1
+                for (int c = group * PW; c < it.rows; c += 2 * PW) {
+                    int v[MT][PW];
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        uint32_t u[32];
-                        tmem_ld_32x32b_x16(tacc + (uint32_t)(mt * N + c), u);
-                        tmem_ld_wait();
+                    for (int mt = 0; mt < MT; ++mt) tmem_ld_piece(tacc + (uint32_t)(mt * N + c), v[mt]);
+                    tmem_ld_wait();
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (c + j < it.rows) part[((c + j) * MT + mt) * 128 + ch] = (int)u[j];
-                    }
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int j = 0; j < PW; ++j)
+                            if (c + j < it.rows) part[((c + j) * MT + mt) * 128 + ch] = v[mt][j];
+                }
             }
             buf ^= 1;
             if (buf == 0) bph ^= 1u;
         }
     }
-    if (a.CS > 1 && S > 1) {
+    if (S > 1) {
         // (S is the same in every block: one tile each, or none)
-        cluster_barrier_sync();
-        if (warp >= 4 && first < tiles && sh.abort == 0) {
-            const int q = warp & 3, group = (warp - 4) >> 2, ch = q * 32 + lane;
-            const XiItem it = xi_item(sh, a.E, N, first);
-            uint32_t parity = 0;
+        const int q = warp & 3, group = (warp - 4) >> 2, ch = q * 32 + lane;
+        float si[MT], bi[MT], sx = 0.f, gt = 0.f;
+        int c0 = 0, n = 0, tk = 0;
+        size_t pair = 0;
+        if (warp >= 4 && warp < 12 && first < tiles) {
             // this block's columns, half of them for each warp group (at most 16)
-            const int per = N / S, c0 = sub * per + group * ((per + 1) / 2);
-            const int c1 = min(group == 0 ? c0 + (per + 1) / 2 : (sub + 1) * per, it.rows);
-            const int n = max(0, c1 - c0);
-            if (n > 0) {
-                const size_t pair = (size_t)it.e * a.w.Tcap + it.base + c0;
-                float si[MT], bi[MT], sx = 0.f, gt = 0.f;
+            const XiItem it = xi_item(sh, a.E, first);
+            const int per = N / S, half = (per + 1) / 2;
+            c0 = sub * per + group * half;
+            n = max(0, min(group == 0 ? c0 + half : (sub + 1) * per, it.rows) - c0);
+            pair = (size_t)it.e * a.w.Tcap + it.base + c0;
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    si[mt] = __ldg(a.s_in + (size_t)it.e * a.d_e + mt * 128 + ch);
-                    bi[mt] = a.b_in != nullptr ? __ldg(a.b_in + (size_t)it.e * a.d_e + mt * 128 + ch) : 0.f;
+            for (int mt = 0; mt < MT; ++mt) {
+                si[mt] = __ldg(a.s_in + (size_t)it.e * a.d_e + mt * 128 + ch);
+                bi[mt] = a.b_in != nullptr ? __ldg(a.b_in + (size_t)it.e * a.d_e + mt * 128 + ch) : 0.f;
+            }
+            if ((lane & 15) < n) {
+                tk = __ldcg(a.w.list + pair + (lane & 15));
+                sx = __ldcg(a.w.sx + tk);
+                gt = __ldg(a.gates + (size_t)tk * a.E + it.e);
+            }
+        }
+        cluster_barrier_sync();
+        if (n > 0 && sh.abort == 0) {
+            uint32_t parity = 0;
+            const uint32_t off = smem_u32(smem) + (uint32_t)(c0 * MT * 128 + ch) * 4u;
+#pragma unroll 1
+            for (int b = 0; b < n; b += PWX) {
+                // (at most four blocks share a tile; all their partial sums in flight at once)
+                int u[4][MT][PWX], v[MT][PWX];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const uint32_t rp = mapa_shared(off, (uint32_t)(crank - sub + (r < S ? r : 0)));
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int j = 0; j < PWX; ++j)
+                            u[r][mt][j] = r < S && b + j < n
+                                              ? ld_shared_cluster_s32(rp + (uint32_t)(((b + j) * MT + mt) * 512)) : 0;
                 }
-                if ((lane & 15) < n) {
-                    const int t = __ldcg(a.w.list + pair + (lane & 15));
-                    sx = __ldcg(a.w.sx + t);
-                    gt = __ldg(a.gates + (size_t)t * a.E + it.e);
-                }
-                int v[MT][16];
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
+                for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        v[mt][j] = 0;
-                        if (j < n) {
-                            const uint32_t off = smem_u32(smem) + (uint32_t)(((c0 + j) * MT + mt) * 128 + ch) * 4u;
-                            for (int r = 0; r < S; ++r)
-                                v[mt][j] += ld_shared_cluster_s32(mapa_shared(off, (uint32_t)(crank - sub + r)));
-                        }
-                    }
-                xi_finish<MT>(a, sh, v, n, it.e, pair, sx, gt, si, bi, group, q, lane, parity);
+                    for (int j = 0; j < PWX; ++j) v[mt][j] = u[0][mt][j] + u[1][mt][j] + u[2][mt][j] + u[3][mt][j];
+                // (lane i of the piece: column b + i, held by lane b + i)
+                const int from = (b + lane) & 15;
+                xi_finish<MT, PWX>(a, sh, v, min(PWX, n - b), pair + b, __shfl_sync(0xffffffffu, tk, from),
+                                  __shfl_sync(0xffffffffu, sx, from), __shfl_sync(0xffffffffu, gt, from), si, bi, group,
+                                  q, lane, parity);
             }
         }
         cluster_barrier_sync();   // no block leaves while its partial sums may be read
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 2) tmem_dealloc(tmem, cols);
+    if (warp == 1) tmem_dealloc(tmem, cols);
 }
 
 // -------------------------------------------------------------- experts_out --
@@ -469,11 +573,22 @@ namespace {
 
 constexpr int kXoMaxStages = 10;
 constexpr int kXoNB = 64;        // pairs of one expert multiplied at a time, at most
-constexpr int kXoAcc = 4;        // accumulators in TMEM
+constexpr int kXoGroups = 2;     // epilogue warp groups: each owns that part of the tile's tokens
+constexpr int kXoThreads = 256 + 128 * kXoGroups;
+constexpr int kXoAcc = 6;        // accumulators in TMEM, and lists of their columns
+constexpr int kXoTmem = 512;     // columns: the accumulators', and room behind the last for a whole piece
 constexpr int kXoMaxEnt = 1024;
 
+// An entry's columns by warp group: (byte offset of the token's row of sums, factor).
+struct alignas(16) XoMeta {
+    uint2 col[kXoGroups][kXoNB + 8];
+    float gate[kXoGroups][kXoNB + 8];
+    float so[128], bo[128];                  // the slab's channel scales and biases
+    int2 span[kXoGroups];                    // first column, columns
+};
+
 struct alignas(16) XoShared {
-    uint64_t full[kXoMaxStages];
+    uint64_t full[2][kXoMaxStages];          // weight tile, pairs' rows landed (bytes)
     uint64_t empty[kXoMaxStages];
     uint64_t acc_full[kXoAcc];
     uint64_t acc_empty[kXoAcc];
@@ -482,50 +597,81 @@ struct alignas(16) XoShared {
     volatile int abort;
     int n_ent;
     uint32_t ent[kXoMaxEnt];                 // expert << 24 | (pairs - 1) << 16 | first pair in its list
-    alignas(16) int2 meta[8][kXoNB];         // by epilogue warp: row offset of the token, factor bits
-    float gate[8][kXoNB];
+    XoMeta meta[kXoAcc];
 };
+
+// Eight columns of an accumulator scaled and added to their tokens' rows of sums (`my`: this
+// channel's word of row 0).  The columns of one entry are different tokens (but for the
+// spare row's, whose sum nobody reads), so all loads go before the stores.
+__device__ __forceinline__ void xo_add(uint32_t taddr, const uint2* col, const float* gate, uint32_t my, float so,
+                                       float bo, bool biased) {
+    uint32_t v[8], at[8];
+    float f[8], s[8];
+    tmem_ld_32x32b_x8(taddr, v);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const uint4 u = *reinterpret_cast<const uint4*>(col + i);
+        at[i] = my + u.x;
+        f[i] = __uint_as_float(u.y);
+        at[i + 1] = my + u.z;
+        f[i + 1] = __uint_as_float(u.w);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] = ld_shared_f32(at[i]);
+    if (biased) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] = fmaf(gate[i], bo, s[i]);
+    }
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) st_shared_f32(at[i], fmaf((float)(int)v[i] * so, f[i], s[i]));
+}
 
 }  // namespace
 
-__global__ void __launch_bounds__(kXThreads, 1)
-int8_experts_out_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_h,
+__global__ void __launch_bounds__(kXoThreads, 1)
+int8_experts_out_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_h16,
+                        const __grid_constant__ CUtensorMap tm_h32, const __grid_constant__ CUtensorMap tm_h64,
                         const X8Out a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int NB = a.NB, TT = a.TT, S = a.S;
     const int stage_bytes = kXTile + NB * 128;
-    float* acc = reinterpret_cast<float*>(smem + (size_t)a.stages * stage_bytes);   // [TT][128]
-    XoShared& sh = *reinterpret_cast<XoShared*>(reinterpret_cast<uint8_t*>(acc) + (size_t)TT * 512);
+    float* acc = reinterpret_cast<float*>(smem + (size_t)a.stages * stage_bytes);   // [TT + 1][128]
+    XoShared& sh = *reinterpret_cast<XoShared*>(reinterpret_cast<uint8_t*>(acc) + (size_t)(TT + 1) * 512);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = S > 1 ? (int)cluster_ctarank() : 0;
     const int item = (int)blockIdx.x / S, slab = item % a.slabs, t0 = item / a.slabs * TT;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < a.stages; ++i) {
-            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.full[0][i], 1);
+            mbar_init(&sh.full[1][i], 1);
             mbar_init(&sh.empty[i], 1);
         }
         for (int i = 0; i < kXoAcc; ++i) {
-            mbar_init(&sh.acc_full[i], 1);
-            mbar_init(&sh.acc_empty[i], 8);
+            mbar_init(&sh.acc_full[i], 2);                 // the MMAs and the list of columns
+            mbar_init(&sh.acc_empty[i], 4 * kXoGroups);
         }
         mbar_init(&sh.mma_done, 1);
         fence_mbar_init();
         sh.abort = 0;
         prefetch_tmap(&tm_w);
-        prefetch_tmap(&tm_h);
+        prefetch_tmap(&tm_h16);
+        prefetch_tmap(&tm_h32);
+        prefetch_tmap(&tm_h64);
     }
     if (warp == 2) {
-        tmem_alloc(&sh.tmem_base, kXoAcc * kXoNB);
+        tmem_alloc(&sh.tmem_base, kXoTmem);
         tmem_relinquish();
     }
-    for (int i = threadIdx.x; i < TT * 32; i += kXThreads) reinterpret_cast<float4*>(acc)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = threadIdx.x; i < TT * 32; i += kXoThreads) reinterpret_cast<float4*>(acc)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     griddep_wait();
     griddep_launch_dependents();
     if (warp == 3) {
         // the tile's pairs, by expert, in pieces of at most NB
         const int c0 = t0 >> 5, c1 = min(a.w.C32, (t0 + TT) >> 5);
+        const int status = __ldcg(&a.ctl->status);
         int lo[8], hi[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -539,6 +685,7 @@ int8_experts_out_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_c
         int run = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
+            if (32 * i >= a.E) break;
             const int ne = (hi[i] - lo[i] + NB - 1) / NB;
             int inc = ne;
 #pragma unroll
@@ -555,7 +702,7 @@ int8_experts_out_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_c
         }
         if (lane == 0) {
             sh.n_ent = run;
-            if (__ldcg(&a.ctl->status) != 0) sh.abort = 1;
+            if (status != 0) sh.abort = 1;
         }
     }
     tc_fence_before();
@@ -566,24 +713,36 @@ int8_experts_out_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_c
     const int ents = sh.abort ? 0 : sh.n_ent;
     const int m0 = ents * rank / S, m1 = ents * (rank + 1) / S;
 
-    if (warp == 0) {
+    if (warp == 0 || warp == 2) {
+        // Warp 0 loads weight tiles, warp 2 the pairs' rows of h: one thread issues a TMA
+        // copy every few hundred cycles, so the two operands have an issuer each.
         if (lane == 0) {
+            uint64_t* const full = sh.full[warp >> 1];
             const uint64_t pol = policy_evict_normal();
             int st = 0, issued = 0;
             uint32_t ph = 0;
             bool ok = true;
             for (int m = m0; m < m1 && ok; ++m) {
                 const uint32_t en = sh.ent[m];
-                const int e = (int)(en >> 24), n16 = (int)((en >> 16 & 255u) + 16) >> 4;
+                const int e = (int)(en >> 24), n = (int)(en >> 16 & 255u) + 1;
                 const int row = e * a.w.Tcap + (int)(en & 0xffffu);
                 for (int kb = 0; kb < a.KBe; ++kb) {
                     ok = wait_bar(&sh.empty[st], ph ^ 1u, limit, &sh.abort, a.ctl, kWaitEmpty);
                     if (!ok) break;
                     uint8_t* sp = smem + (size_t)st * stage_bytes;
-                    mbar_arrive_expect_tx(&sh.full[st], (uint32_t)(kXTile + n16 * 2048));
-                    tma_load_2d(sp, &tm_w, &sh.full[st], kb * 128, e * a.d_h + slab * 128, pol);
-                    for (int i = 0; i < n16; ++i)
-                        tma_load_2d(sp + kXTile + i * 2048, &tm_h, &sh.full[st], kb * 128, row + 16 * i, pol);
+                    if (warp == 0) {
+                        mbar_arrive_expect_tx(&full[st], (uint32_t)kXTile);
+                        tma_load_2d(sp, &tm_w, &full[st], kb * 128, e * a.d_h + slab * 128, pol);
+                    } else if (n <= 16) {
+                        mbar_arrive_expect_tx(&full[st], 16u * 128u);
+                        tma_load_2d(sp + kXTile, &tm_h16, &full[st], kb * 128, row, pol);
+                    } else if (n <= 32) {
+                        mbar_arrive_expect_tx(&full[st], 32u * 128u);
+                        tma_load_2d(sp + kXTile, &tm_h32, &full[st], kb * 128, row, pol);
+                    } else {
+                        mbar_arrive_expect_tx(&full[st], 64u * 128u);
+                        tma_load_2d(sp + kXTile, &tm_h64, &full[st], kb * 128, row, pol);
+                    }
                     ++issued;
                     if (++st == a.stages) {
                         st = 0;
@@ -591,27 +750,39 @@ int8_experts_out_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_c
                     }
                 }
             }
+            // every load issued has landed before the block may end
             const int in_ring = min(issued, a.stages);
             for (int i = 0; i < in_ring; ++i) {
                 st = st == 0 ? a.stages - 1 : st - 1;
-                wait_bar_drain(&sh.full[st], (uint32_t)(((issued - 1 - i) / a.stages) & 1), limit, a.ctl);
+                wait_bar_drain(&full[st], (uint32_t)(((issued - 1 - i) / a.stages) & 1), limit, a.ctl);
             }
         }
         __syncwarp();
     } else if (warp == 1) {
+        // One entry after another; the barriers of the next stage and accumulator are tested
+        // before the present one's MMAs are issued, so that in the steady state nothing
+        // is waited for (waiting in turn for each made 600 cycles an entry).
         const uint64_t desc0 = sw128_kmajor_desc(smem_u32(smem));
         int st = 0, buf = 0;
         uint32_t ph = 0, bph = 0;
         bool ok = true;
+        uint32_t got_w = 0, got_h = 0, got_a = 0;
         for (int m = m0; m < m1 && ok; ++m) {
             const uint32_t idesc = idesc_i8_s32(128, (int)((sh.ent[m] >> 16 & 255u) + 16) & ~15);
-            ok = wait_bar_warp(&sh.acc_empty[buf], bph ^ 1u, limit, &sh.abort, a.ctl, kWaitAccEmpty);
+            ok = wait_tested(got_a, &sh.acc_empty[buf], bph ^ 1u, limit, &sh.abort, a.ctl, kWaitAccEmpty);
             if (!ok) break;
-            tc_fence_after();
+            const int nbuf = buf + 1 == kXoAcc ? 0 : buf + 1;
+            const uint32_t nbph = nbuf == 0 ? bph ^ 1u : bph;
             for (int kb = 0; kb < a.KBe; ++kb) {
-                ok = wait_bar_warp(&sh.full[st], ph, limit, &sh.abort, a.ctl, kWaitFullH);
+                ok = wait_tested(got_w, &sh.full[0][st], ph, limit, &sh.abort, a.ctl, kWaitFullW) &&
+                     wait_tested(got_h, &sh.full[1][st], ph, limit, &sh.abort, a.ctl, kWaitFullH);
                 if (!ok) break;
                 tc_fence_after();
+                const int nst = st + 1 == a.stages ? 0 : st + 1;
+                const uint32_t nph = nst == 0 ? ph ^ 1u : ph;
+                got_w = mbar_test_wait(&sh.full[0][nst], nph);
+                got_h = mbar_test_wait(&sh.full[1][nst], nph);
+                if (kb == a.KBe - 1) got_a = mbar_test_wait(&sh.acc_empty[nbuf], nbph ^ 1u);
                 if (elect_one()) {
                     const uint64_t ad = desc0 + (uint64_t)((uint32_t)st * (uint32_t)stage_bytes >> 4);
                     const uint64_t bd = ad + (kXTile >> 4);
@@ -622,85 +793,111 @@ int8_experts_out_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_c
                     if (kb == a.KBe - 1) umma_commit(&sh.acc_full[buf]);
                 }
                 __syncwarp();
-                if (++st == a.stages) {
-                    st = 0;
-                    ph ^= 1u;
-                }
+                st = nst;
+                ph = nph;
             }
-            if (++buf == kXoAcc) {
-                buf = 0;
-                bph ^= 1u;
-            }
+            buf = nbuf;
+            bph = nbph;
         }
         if (elect_one()) umma_commit(&sh.mma_done);
         __syncwarp();
         if (lane == 0) wait_bar_drain(&sh.mma_done, 0u, limit, a.ctl);
         __syncwarp();
-    } else if (warp >= 4) {
-        // A warp group owns half of the tile's tokens (a thread one channel of them), so no
+    } else if (warp >= 4 && warp < 8) {
+        // What the epilogue needs of each entry (the four warps in turn, reading kAhead of their
+        // entries ahead: the loads' latency is several entries' time): the channels' scales
+        // and biases, and every epilogue group's columns as (byte offset of the token's row of
+        // sums, factor).  Tokens ascend, so a group's columns are neighbours.  Columns of the
+        // spare row follow each list: the epilogue takes eight at a time.
+        constexpr int kAhead = 2;
+        float4 p0[kAhead], p1[kAhead], so[kAhead], bo[kAhead];
+        const bool biased = a.b_out != nullptr;
+        auto fetch = [&](int m, int k) {
+            if (m >= m1) return;
+            const uint32_t en = sh.ent[m];
+            const int n = (int)(en >> 16 & 255u) + 1;
+            const float4* src = a.w.pair + (size_t)(en >> 24) * a.w.Tcap + (en & 0xffffu);
+            if (lane < n) p0[k] = __ldcg(src + lane);
+            if (lane + 32 < n) p1[k] = __ldcg(src + lane + 32);
+            const size_t ch = (size_t)(en >> 24) * a.d_h + slab * 128 + lane * 4;
+            so[k] = __ldg(reinterpret_cast<const float4*>(a.s_out + ch));
+            if (biased) bo[k] = __ldg(reinterpret_cast<const float4*>(a.b_out + ch));
+        };
+        const int mw = m0 + warp - 4;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            p0[k] = p1[k] = so[k] = bo[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            fetch(mw + 4 * k, k);
+        }
+        bool ok = true;
+        const int part = 31 - __clz(TT / kXoGroups);   // a group's tokens: 2^part
+        for (int mb = mw; mb < m1 && ok; mb += 4 * kAhead) {
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int m = mb + 4 * k;
+                if (m >= m1) break;
+                const int slot = (m - m0) % kXoAcc;
+                ok = wait_bar_warp(&sh.acc_empty[slot], (uint32_t)((m - m0) / kXoAcc & 1) ^ 1u, limit, &sh.abort, a.ctl,
+                                   kWaitEmpty);
+                if (!ok) break;
+                const int n = (int)(sh.ent[m] >> 16 & 255u) + 1;
+                XoMeta& mt = sh.meta[slot];
+                reinterpret_cast<float4*>(mt.so)[lane] = so[k];
+                if (biased) reinterpret_cast<float4*>(mt.bo)[lane] = bo[k];
+                const int r0 = __float_as_int(p0[k].x) & (TT - 1), r1 = __float_as_int(p1[k].x) & (TT - 1);
+                const int g0 = lane < n ? r0 >> part : kXoGroups, g1 = lane + 32 < n ? r1 >> part : kXoGroups;
+                int from = 0;   // columns before group g
+#pragma unroll
+                for (int g = 0; g < kXoGroups; ++g) {
+                    const int cn = __popc(__ballot_sync(0xffffffffu, g0 == g)) + __popc(__ballot_sync(0xffffffffu, g1 == g));
+                    if (g0 == g) {
+                        mt.col[g][lane - from] = make_uint2((uint32_t)r0 * 512u, __float_as_uint(p0[k].y));
+                        mt.gate[g][lane - from] = p0[k].z;
+                    }
+                    if (g1 == g) {
+                        mt.col[g][lane + 32 - from] = make_uint2((uint32_t)r1 * 512u, __float_as_uint(p1[k].y));
+                        mt.gate[g][lane + 32 - from] = p1[k].z;
+                    }
+                    if (lane < 8) {
+                        mt.col[g][cn + lane] = make_uint2((uint32_t)TT * 512u, 0u);
+                        mt.gate[g][cn + lane] = 0.f;
+                    }
+                    if (lane == g) mt.span[g] = make_int2(from, cn);
+                    from += cn;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.acc_full[slot]);
+                fetch(m + 4 * kAhead, k);
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 8) {
+        // A warp group owns its part of the tile's tokens (a thread one channel of them), so no
         // sum is touched by two warps and the groups need not meet.
-        const int q = warp & 3, group = (warp - 4) >> 2, ch = q * 32 + lane, o = slab * 128 + ch;
-        int2* meta = sh.meta[warp - 4];
-        float* mgate = sh.gate[warp - 4];
+        const int q = warp & 3, group = (warp - 8) >> 2, ch = q * 32 + lane;
         const bool biased = a.b_out != nullptr;
         int buf = 0;
         uint32_t bph = 0;
-        uint8_t* const my = reinterpret_cast<uint8_t*>(acc) + ch * 4;
+        const uint32_t my = smem_u32(acc) + (uint32_t)ch * 4u;
+        uint32_t got = 0;
         for (int m = m0; m < m1; ++m) {
-            const uint32_t en = sh.ent[m];
-            const int e = (int)(en >> 24), n = (int)(en >> 16 & 255u) + 1;
-            const size_t pair = (size_t)e * a.w.Tcap + (en & 0xffffu);
-            const float so = __ldg(a.s_out + (size_t)e * a.d_h + o);
-            const float bo = biased ? __ldg(a.b_out + (size_t)e * a.d_h + o) : 0.f;
-            int below = 0;   // columns whose tokens are in the first half (tokens ascend)
-            __syncwarp();
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int c = lane + 32 * u;
-                int tl = TT;
-                if (c < n) {
-                    tl = __ldcg(a.w.list + pair + c) - t0;
-                    const float2 f = __ldcg(a.w.fpair + pair + c);
-                    meta[c] = make_int2(tl * 512, __float_as_int(f.x));
-                    mgate[c] = f.y;
-                }
-                below += __popc(__ballot_sync(0xffffffffu, tl < TT / 2));
-            }
-            __syncwarp();
-            const int ca = group == 0 ? 0 : below, cb = group == 0 ? below : n;
-            if (!wait_bar_warp(&sh.acc_full[buf], bph, limit, &sh.abort, a.ctl, kWaitAccFull)) break;
+            if (!wait_tested(got, &sh.acc_full[buf], bph, limit, &sh.abort, a.ctl, kWaitAccFull)) break;
             tc_fence_after();
-            const uint32_t tacc = tmem + (uint32_t)(buf * kXoNB) + ((uint32_t)(q * 32) << 16);
-            for (int c = ca & ~15; c < cb; c += 16) {
-                uint32_t v[32];
-                tmem_ld_32x32b_x16(tacc + (uint32_t)c, v);
-                tmem_ld_wait();
-#pragma unroll
-                for (int b = 0; b < 16; b += 8) {
-                    int2 mt[8];
-                    float s[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        mt[i] = meta[c + b + i];
-                        if (c + b + i >= ca && c + b + i < cb) s[i] = *reinterpret_cast<float*>(my + mt[i].x);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        if (c + b + i >= ca && c + b + i < cb) {
-                            float r = fmaf((float)(int)v[b + i] * so, __int_as_float(mt[i].y), s[i]);
-                            if (biased) r = fmaf(mgate[c + b + i], bo, r);
-                            *reinterpret_cast<float*>(my + mt[i].x) = r;
-                        }
-                    }
-                }
-            }
+            const int nbuf = buf + 1 == kXoAcc ? 0 : buf + 1;
+            const uint32_t nbph = nbuf == 0 ? bph ^ 1u : bph;
+            got = mbar_test_wait(&sh.acc_full[nbuf], nbph);
+            const int2 span = sh.meta[buf].span[group];
+            const uint2* col = sh.meta[buf].col[group];
+            const float* gate = sh.meta[buf].gate[group];
+            const float so = sh.meta[buf].so[ch], bo = biased ? sh.meta[buf].bo[ch] : 0.f;
+            const uint32_t tacc = tmem + (uint32_t)(buf * kXoNB + span.x) + ((uint32_t)(q * 32) << 16);
+#pragma unroll 1
+            for (int c = 0; c < span.y; c += 8) xo_add(tacc + (uint32_t)c, col + c, gate + c, my, so, bo, biased);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);
-            if (++buf == kXoAcc) {
-                buf = 0;
-                bph ^= 1u;
-            }
+            buf = nbuf;
+            bph = nbph;
         }
     }
     // y: the blocks of the cluster add their rows in rank order, each its share of the tokens
@@ -708,7 +905,7 @@ int8_experts_out_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_c
     else __syncthreads();
     if (sh.abort == 0) {
         const int ra = TT * rank / S, rb = min(TT * (rank + 1) / S, a.T - t0);
-        for (int i = ra * 16 + (int)threadIdx.x; i < rb * 16; i += kXThreads) {
+        for (int i = ra * 16 + (int)threadIdx.x; i < rb * 16; i += kXoThreads) {
             float f[8];
             const float* p = acc + i * 8;
             if (S == 1) {
@@ -736,7 +933,7 @@ int8_experts_out_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_c
     if (S > 1) cluster_barrier_sync();   // no block leaves while its rows may be read
     tc_fence_before();
     __syncthreads();
-    if (warp == 2) tmem_dealloc(tmem, kXoAcc * kXoNB);
+    if (warp == 2) tmem_dealloc(tmem, kXoTmem);
 }
 
 // ----------------------------------------------------------------- launches --
@@ -762,55 +959,58 @@ cudaLaunchConfig_t x8_config(int grid, int threads, size_t smem, cudaStream_t s,
 constexpr int kMaxSmem = 227 * 1024;
 
 template <int MT>
-cudaError_t launch_in(const X8In& a, const CUtensorMap* maps, int grid, size_t smem, cudaStream_t s) {
+cudaError_t launch_in(const X8In& a, const CUtensorMap& map, int grid, size_t smem, cudaStream_t s) {
     auto kern = int8_experts_in_kernel<MT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute at[2];
-    cudaLaunchConfig_t cfg = x8_config(grid, kXThreads, smem, s, at, a.CS);
-    return cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], a);
+    cudaLaunchConfig_t cfg = x8_config(grid, kXiThreads, smem, s, at, a.CS);
+    return cudaLaunchKernelEx(&cfg, kern, map, a);
 }
 
 }  // namespace
 
 cudaError_t launch_int8_prepare(const __nv_bfloat16* x, const float* gates, int T, int d_h, int E, const X8Bufs& w,
                                 cudaStream_t s) {
+    const QuantPlan p = quantize_plan(T, d_h, 2);
+    const int per = kQThreads / p.W;
     cudaLaunchAttribute at[2];
-    cudaLaunchConfig_t cfg = x8_config(T + E, quantize_threads(d_h, 2), 0, s, at, 1);
-    return quantize_one_pass(d_h, 2) ? cudaLaunchKernelEx(&cfg, int8_prepare_kernel<true>, x, gates, T, d_h, E, w)
-                                     : cudaLaunchKernelEx(&cfg, int8_prepare_kernel<false>, x, gates, T, d_h, E, w);
+    cudaLaunchConfig_t cfg = x8_config(E + (T + per - 1) / per, kQThreads, 0, s, at, 1);
+    if (p.C == 0) return cudaLaunchKernelEx(&cfg, int8_prepare_kernel<0>, x, gates, T, d_h, E, p.W, w);
+    if (p.C == 2) return cudaLaunchKernelEx(&cfg, int8_prepare_kernel<2>, x, gates, T, d_h, E, p.W, w);
+    return cudaLaunchKernelEx(&cfg, int8_prepare_kernel<8>, x, gates, T, d_h, E, p.W, w);
 }
 
 // Tokens per tile and blocks per cluster.  A tile of all an expert's tokens reads its
 // weight once, so N grows with T, up to what two accumulators of all d_e rows leave of
-// TMEM (2 * d_e / 128 * N <= 512 columns) and a gather of one warp (128 rows).  Where
+// TMEM (2 * d_e / 128 * N <= 512 columns).  Where
 // the tiles may be fewer than the SMs, clusters let several blocks share a tile.
-cudaError_t launch_int8_experts_in(X8In a, const CUtensorMap* maps, int sms, cudaStream_t s) {
+cudaError_t launch_int8_experts_in(X8In a, const CUtensorMap& map, int sms, cudaStream_t s) {
     const int MT = a.d_e / 128, stage = MT * kXTile + a.N * 128;
     a.stages = kXRing / stage < kXMaxStages ? kXRing / stage : kXMaxStages;
     const size_t smem = 1024 + (size_t)a.stages * stage + sizeof(XiShared);
-    // (clusters of 8 do not fill every SM: 16 of them fit)
-    const int grid = a.CS == 8 ? 128 : sms / a.CS * a.CS;
+    const int fit = a.CS > 1 ? int8_cluster_capacity(a.CS) * a.CS : sms;
+    const int grid = fit > 0 ? fit : sms / a.CS * a.CS;
     switch (MT) {
-        case 1: return launch_in<1>(a, maps, grid, smem, s);
-        case 2: return launch_in<2>(a, maps, grid, smem, s);
-        case 3: return launch_in<3>(a, maps, grid, smem, s);
-        default: return launch_in<4>(a, maps, grid, smem, s);
+        case 1: return launch_in<1>(a, map, grid, smem, s);
+        case 2: return launch_in<2>(a, map, grid, smem, s);
+        case 3: return launch_in<3>(a, map, grid, smem, s);
+        default: return launch_in<4>(a, map, grid, smem, s);
     }
 }
 
 cudaError_t launch_int8_experts_out(X8Out a, const CUtensorMap* maps, cudaStream_t s) {
-    const int stage = kXTile + a.NB * 128;
-    const int room = (kMaxSmem - 1024 - (int)sizeof(XoShared) - a.TT * 512) / stage;
+    const int stage = kXTile + (a.NB <= 16 ? 16 : a.NB <= 32 ? 32 : 64) * 128;
+    const int room = (kMaxSmem - 1024 - (int)sizeof(XoShared) - (a.TT + 1) * 512) / stage;
     a.stages = room < kXoMaxStages ? room : kXoMaxStages;
-    const size_t smem = 1024 + (size_t)a.stages * stage + (size_t)a.TT * 512 + sizeof(XoShared);
+    const size_t smem = 1024 + (size_t)a.stages * stage + (size_t)(a.TT + 1) * 512 + sizeof(XoShared);
     auto kern = int8_experts_out_kernel;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute at[2];
     const int grid = a.slabs * ((a.T + a.TT - 1) / a.TT) * a.S;
-    cudaLaunchConfig_t cfg = x8_config(grid, kXThreads, smem, s, at, a.S);
-    return cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], a);
+    cudaLaunchConfig_t cfg = x8_config(grid, kXoThreads, smem, s, at, a.S);
+    return cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], maps[3], a);
 }
 
 }  // namespace bffn

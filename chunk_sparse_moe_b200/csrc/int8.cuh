@@ -28,6 +28,14 @@ __host__ __device__ constexpr uint32_t idesc_i8_s32(int M, int N) {
            | (static_cast<uint32_t>(M >> 4) << 24);    // M / 16
 }
 
+// A warp's wait for a barrier phase that it tested some time ago (`tested`: the test's
+// result, so that its latency runs under other work); false after a timeout or abort.
+__device__ __forceinline__ bool wait_tested(uint32_t tested, uint64_t* bar, uint32_t parity, uint64_t limit_ns,
+                                            volatile int* abort, Ctl* ctl, int32_t detail) {
+    if (__all_sync(0xffffffffu, tested != 0)) return true;
+    return wait_bar_warp(bar, parity, limit_ns, abort, ctl, detail);
+}
+
 __device__ __forceinline__ int ld_shared_cluster_s32(uint32_t cluster_addr) {
     int v;
     asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
@@ -65,101 +73,125 @@ __device__ __forceinline__ int quantize_exact(float v, const RowScale& r) {
     if (fabsf(fabsf(p - q) - 0.5f) < 1e-4f) q = (float)rint((double)v * 127.0 / (double)r.amax);
     return (int)q;
 }
-__device__ __forceinline__ uint32_t pack4_i8(int a, int b, int c, int d) {
-    return (uint32_t)(a & 255) | (uint32_t)(b & 255) << 8 | (uint32_t)(c & 255) << 16 | (uint32_t)d << 24;
-}
-
 __device__ __forceinline__ float as_f32(float v) { return v; }
 __device__ __forceinline__ float as_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 
-// 16 bytes of a row as fp32 values
-__device__ __forceinline__ void load_chunk(const __nv_bfloat16* p, float (&f)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
+// The magnitude of the largest of 16 bytes of values, as bits of an fp32 (a bf16 is its
+// upper half); NaN above infinity above numbers.
+template <typename T>
+__device__ __forceinline__ uint32_t chunk_max(uint32_t m, const uint4& u) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
-        f[2 * i] = __low2float(h);
-        f[2 * i + 1] = __high2float(h);
+        if constexpr (sizeof(T) == 2) m = __vmaxu2(m, w[i] & 0x7fff7fffu);   // (two running maxima)
+        else m = max(m, w[i] & 0x7fffffffu);
     }
-}
-__device__ __forceinline__ void load_chunk(const float* p, float (&f)[4]) {
-    const float4 u = *reinterpret_cast<const float4*>(p);
-    f[0] = u.x;
-    f[1] = u.y;
-    f[2] = u.z;
-    f[3] = u.w;
-}
-__device__ __forceinline__ void store_q(int8_t* p, const int (&q)[8]) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack4_i8(q[0], q[1], q[2], q[3]), pack4_i8(q[4], q[5], q[6], q[7]));
-}
-__device__ __forceinline__ void store_q(int8_t* p, const int (&q)[4]) {
-    *reinterpret_cast<uint32_t*>(p) = pack4_i8(q[0], q[1], q[2], q[3]);
-}
-
-// The block's largest |v| as bits; red: one word per warp, free again on return.
-__device__ __forceinline__ uint32_t block_max_bits(uint32_t v, uint32_t* red) {
-    v = __reduce_max_sync(0xffffffffu, v);
-    const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    if ((threadIdx.x & 31) == 0) red[warp] = v;
-    __syncthreads();
-    uint32_t m = 0;
-    for (int w = 0; w < nw; ++w) m = max(m, red[w]);
-    __syncthreads();
     return m;
 }
+template <typename T>
+__device__ __forceinline__ uint32_t chunk_max_bits(uint32_t m) {
+    return sizeof(T) == 2 ? max(m << 16, m & 0xffff0000u) : m;
+}
+template <typename T>
+__device__ __forceinline__ float chunk_value(const uint4& u, int i) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    if constexpr (sizeof(T) == 2) return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+    else return __uint_as_float(w[i]);
+}
 
-constexpr int kQChunks = 4;   // 16-byte chunks a thread keeps in registers
-
-// One block rounds one row of K values.  VEC: K values in whole 16-byte chunks,
-// K <= chunk values * kQChunks * threads, read once; otherwise two passes.
-template <typename T, bool VEC>
-__device__ __forceinline__ void quantize_row(const T* __restrict__ v, int K, int8_t* __restrict__ q, float* scale,
-                                             uint32_t* red) {
+// 16 bytes of a row (V values) in 8 bits.  v * inv is rounded by adding 1.5 * 2^23 (the
+// whole number is the sum's low byte); what was rounded off tells whether a value is near
+// the border of two whole numbers, and such a chunk is done again exactly.
+template <typename T>
+__device__ __forceinline__ void quantize_chunk(const uint4& u, const RowScale& r, int8_t* out) {
     constexpr int V = 16 / (int)sizeof(T);
-    const int tid = threadIdx.x, nt = blockDim.x;
-    if constexpr (VEC) {
-        float f[kQChunks][V];
-        uint32_t m = 0;
+    constexpr float kMagic = 12582912.f;
+    uint32_t b[V];
+    float worst = 0.f;
 #pragma unroll
-        for (int c = 0; c < kQChunks; ++c) {
-            const int k = (c * nt + tid) * V;
-            if (k < K) {
-                load_chunk(v + k, f[c]);
+    for (int i = 0; i < V; ++i) {
+        const float v = chunk_value<T>(u, i);
+        const float t = fmaf(v, r.inv, kMagic);
+        b[i] = __float_as_uint(t);
+        worst = fmaxf(worst, fabsf(fmaf(v, r.inv, kMagic - t)));
+    }
+    if (worst > 0.49998f) {   // (inv is off by 2^-24 of itself: the product by 8e-6 at most)
 #pragma unroll
-                for (int i = 0; i < V; ++i) m = max(m, __float_as_uint(f[c][i]) & 0x7fffffffu);
-            }
+        for (int i = 0; i < V; ++i) b[i] = (uint32_t)quantize_exact(chunk_value<T>(u, i), r);
+    }
+    uint32_t p[V / 4];
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i)
+        p[i] = __byte_perm(__byte_perm(b[4 * i], b[4 * i + 1], 0x0040), __byte_perm(b[4 * i + 2], b[4 * i + 3], 0x0040),
+                           0x5410);
+    if constexpr (V == 8) *reinterpret_cast<uint2*>(out) = make_uint2(p[0], p[1]);
+    else *reinterpret_cast<uint32_t*>(out) = p[0];
+}
+
+// W threads (a multiple of 32; thread `t` of them, meeting at named barrier `bar` when
+// they are more than a warp) round one row of K values.  C > 0: K values in whole
+// 16-byte chunks, at most C * W of them, read once and kept in registers.  C == 0: any
+// K, two passes.  red: a word per warp of the group.
+template <typename T, int C>
+__device__ __forceinline__ void quantize_row(const T* __restrict__ v, int K, int8_t* __restrict__ q, float* scale, int W,
+                                             int t, int bar, uint32_t* red) {
+    constexpr int V = 16 / (int)sizeof(T);
+    uint4 u[C > 0 ? C : 1];
+    uint32_t m = 0;
+    if constexpr (C > 0) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            u[c] = make_uint4(0u, 0u, 0u, 0u);
+            if ((c * W + t) * V < K) u[c] = *reinterpret_cast<const uint4*>(v + (c * W + t) * V);
         }
-        const RowScale r = row_scale(block_max_bits(m, red));
-        if (tid == 0) *scale = r.scale;
 #pragma unroll
-        for (int c = 0; c < kQChunks; ++c) {
-            const int k = (c * nt + tid) * V;
+        for (int c = 0; c < C; ++c) m = chunk_max<T>(m, u[c]);
+        m = chunk_max_bits<T>(m);
+    } else {
+        for (int k = t; k < K; k += W) m = max(m, __float_as_uint(as_f32(v[k])) & 0x7fffffffu);
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (W > 32) {
+        if ((t & 31) == 0) red[t >> 5] = m;
+        named_bar_sync(bar, W);
+        for (int w = 0; w < W / 32; ++w) m = max(m, red[w]);
+    }
+    const RowScale r = row_scale(m);
+    if (t == 0) *scale = r.scale;
+    if constexpr (C > 0) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int k = (c * W + t) * V;
             if (k < K) {
-                int o[V];
-#pragma unroll
-                for (int i = 0; i < V; ++i) o[i] = r.inv != 0.f ? quantize_exact(f[c][i], r) : 0;
-                store_q(q + k, o);
+                if (r.inv != 0.f) {
+                    quantize_chunk<T>(u[c], r, q + k);
+                } else if constexpr (V == 8) {
+                    *reinterpret_cast<uint2*>(q + k) = make_uint2(0u, 0u);
+                } else {
+                    *reinterpret_cast<uint32_t*>(q + k) = 0u;
+                }
             }
         }
     } else {
-        uint32_t m = 0;
-        for (int k = tid; k < K; k += nt) m = max(m, __float_as_uint(as_f32(v[k])) & 0x7fffffffu);
-        const RowScale r = row_scale(block_max_bits(m, red));
-        if (tid == 0) *scale = r.scale;
-        for (int k = tid; k < K; k += nt) q[k] = (int8_t)(r.inv != 0.f ? quantize_exact(as_f32(v[k]), r) : 0);
+        for (int k = t; k < K; k += W) q[k] = (int8_t)(r.inv != 0.f ? quantize_exact(as_f32(v[k]), r) : 0);
     }
 }
 
-// Threads of a block that rounds rows of K values, and whether one pass serves.
-inline int quantize_threads(int K, int elem_bytes) {
-    const int chunks = (K * elem_bytes + 15) / 16;
-    const int t = ((chunks + 1) / 2 + 31) / 32 * 32;   // two chunks a thread where the row is long enough
-    return t < 64 ? 64 : (t > 256 ? 256 : t);
-}
-inline bool quantize_one_pass(int K, int elem_bytes) {
+// How a block of 256 threads rounds rows of K values: W threads a row, C chunks of 16
+// bytes a thread (0: two passes).  Few rows are spread over more threads (what counts
+// is the way through one row), many keep a warp to a row where it fits (no barrier).
+constexpr int kQThreads = 256;
+struct QuantPlan {
+    int W, C;
+};
+inline QuantPlan quantize_plan(int rows, int K, int elem_bytes) {
     const int V = 16 / elem_bytes;
-    return K % V == 0 && K <= V * kQChunks * quantize_threads(K, elem_bytes);
+    QuantPlan p{kQThreads, 0};
+    if (K % V != 0 || K / V > 8 * kQThreads) return p;
+    p.C = rows <= 296 && K / V <= 2 * kQThreads ? 2 : 8;
+    p.W = 32;
+    while (p.W * p.C < K / V) p.W *= 2;
+    return p;
 }
 
 }  // namespace bffn

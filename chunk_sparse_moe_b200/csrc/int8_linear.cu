@@ -28,41 +28,48 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <mutex>
+
 #include "int8.cuh"
 #include "launch.h"
 
 namespace bffn {
 
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) quantize_rows_kernel(const T* __restrict__ v, int K, int8_t* __restrict__ q,
-                                                            float* __restrict__ scale) {
+template <typename T, int C>
+__global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(const T* __restrict__ v, int rows, int K, int W,
+                                                                  int8_t* __restrict__ q, float* __restrict__ scale) {
     __shared__ uint32_t red[8];
     griddep_wait();
     griddep_launch_dependents();
-    const size_t row = blockIdx.x;
-    quantize_row<T, VEC>(v + row * K, K, q + row * K, scale + row, red);
+    const int g = threadIdx.x / W;   // the block's group of W threads
+    const long long row = (long long)blockIdx.x * (kQThreads / W) + g;
+    if (row >= rows) return;
+    quantize_row<T, C>(v + row * K, K, q + row * K, scale + row, W, threadIdx.x - g * W, 1 + g, red + g * (W / 32));
 }
 
-cudaError_t launch_quantize_rows(const void* v, bool bf16, int rows, int K, int8_t* q, float* scale, cudaStream_t s) {
-    const int eb = bf16 ? 2 : 4;
+namespace {
+template <typename T>
+cudaError_t launch_quantize_t(const T* v, int rows, int K, int8_t* q, float* scale, cudaStream_t s) {
+    const QuantPlan p = quantize_plan(rows, K, (int)sizeof(T));
+    const int per = kQThreads / p.W;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)rows);
-    cfg.blockDim = dim3((unsigned)quantize_threads(K, eb));
+    cfg.gridDim = dim3((unsigned)((rows + (long long)per - 1) / per));
+    cfg.blockDim = dim3(kQThreads);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    const bool one = quantize_one_pass(K, eb);
-    if (bf16) {
-        auto* p = static_cast<const __nv_bfloat16*>(v);
-        return one ? cudaLaunchKernelEx(&cfg, quantize_rows_kernel<__nv_bfloat16, true>, p, K, q, scale)
-                   : cudaLaunchKernelEx(&cfg, quantize_rows_kernel<__nv_bfloat16, false>, p, K, q, scale);
-    }
-    auto* p = static_cast<const float*>(v);
-    return one ? cudaLaunchKernelEx(&cfg, quantize_rows_kernel<float, true>, p, K, q, scale)
-               : cudaLaunchKernelEx(&cfg, quantize_rows_kernel<float, false>, p, K, q, scale);
+    if (p.C == 0) return cudaLaunchKernelEx(&cfg, quantize_rows_kernel<T, 0>, v, rows, K, p.W, q, scale);
+    if (p.C == 2) return cudaLaunchKernelEx(&cfg, quantize_rows_kernel<T, 2>, v, rows, K, p.W, q, scale);
+    return cudaLaunchKernelEx(&cfg, quantize_rows_kernel<T, 8>, v, rows, K, p.W, q, scale);
+}
+}  // namespace
+
+cudaError_t launch_quantize_rows(const void* v, bool bf16, int rows, int K, int8_t* q, float* scale, cudaStream_t s) {
+    return bf16 ? launch_quantize_t(static_cast<const __nv_bfloat16*>(v), rows, K, q, scale, s)
+                : launch_quantize_t(static_cast<const float*>(v), rows, K, q, scale, s);
 }
 
 namespace {
@@ -179,16 +186,19 @@ int8_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
         const uint32_t idesc = idesc_i8_s32(128, N);
         const uint64_t desc0 = sw128_kmajor_desc(smem_u32(smem));
         int st = 0, buf = 0;
-        uint32_t ph = 0, bph = 0;
+        uint32_t ph = 0, bph = 0, got = 0;
         bool ok = true;
         for (int tile = first; tile < tiles && ok; tile += step) {
             ok = wait_bar_warp(&sh.acc_empty[buf], bph ^ 1u, limit, &sh.abort, a.ctl, kWaitAccEmpty);
             if (!ok) break;
             tc_fence_after();
             for (int kb = kb0; kb < kb1; ++kb) {
-                ok = wait_bar_warp(&sh.full[st], ph, limit, &sh.abort, a.ctl, kWaitFullW);
+                ok = wait_tested(got, &sh.full[st], ph, limit, &sh.abort, a.ctl, kWaitFullW);
                 if (!ok) break;
                 tc_fence_after();
+                const int nst = st + 1 == a.stages ? 0 : st + 1;
+                const uint32_t nph = nst == 0 ? ph ^ 1u : ph;
+                got = mbar_test_wait(&sh.full[nst], nph);   // the next stage's, tested ahead
                 if (elect_one()) {
                     const uint64_t ad = desc0 + (uint64_t)((uint32_t)st * (uint32_t)stage_bytes >> 4);
                     const uint64_t bd = ad + (kIlABytes >> 4);
@@ -199,10 +209,8 @@ int8_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
                     if (kb == kb1 - 1) umma_commit(&sh.acc_full[buf]);
                 }
                 __syncwarp();
-                if (++st == a.stages) {
-                    st = 0;
-                    ph ^= 1u;
-                }
+                st = nst;
+                ph = nph;
             }
             buf ^= 1;
             if (buf == 0) bph ^= 1u;
@@ -220,13 +228,12 @@ int8_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
         for (int tile = first; tile < tiles; tile += step) {
             const int to = tile % a.tiles_o, tt = tile / a.tiles_o;
             const int t0 = tt * N, o = to * 128 + ch;
-            // lanes 0-15 hold the scales of the columns of each of the group's pieces
-            float sx[8];
-#pragma unroll
-            for (int p = 0; p < 8; ++p) {
-                const int t = t0 + half * 16 + 32 * p + (lane & 15);
-                sx[p] = (half * 16 + 32 * p < N && t < a.T) ? __ldcg(a.sx + t) : 0.f;
-            }
+            // lanes 0-15 hold the token scales of a piece's columns
+            auto scales = [&](int c) {
+                const int t = t0 + c + (lane & 15);
+                return c < N && t < a.T ? __ldcg(a.sx + t) : 0.f;
+            };
+            float sx = S == 1 ? scales(half * 16) : 0.f;
             const float sw = o < a.O ? __ldg(a.sw + o) : 0.f;
             const float b = (a.bias != nullptr && o < a.O) ? __ldg(a.bias + o) : 0.f;
             if (!wait_bar_warp(&sh.acc_full[buf], bph, limit, &sh.abort, a.ctl, kWaitAccFull)) break;
@@ -234,24 +241,23 @@ int8_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
             const uint32_t tacc = tmem + (uint32_t)(buf * N) + ((uint32_t)(q * 32) << 16);
             OutT* y = static_cast<OutT*>(a.y) + (size_t)t0 * a.O + o;
             if (S == 1) {
+#pragma unroll 1
+                for (int c = half * 16; c < N; c += 32) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x16(tacc + (uint32_t)c, v);
+                    const float sx0 = sx;
+                    sx = scales(c + 32);
+                    tmem_ld_wait();
+                    if (c + 32 >= N) {   // the group's last piece: its columns are in registers
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);
+                    }
 #pragma unroll
-                for (int p = 0; p < 8; ++p) {
-                    const int c = half * 16 + 32 * p;
-                    if (c < N) {
-                        uint32_t v[32];
-                        tmem_ld_32x32b_x16(tacc + (uint32_t)c, v);
-                        tmem_ld_wait();
-                        if (c + 32 >= N) {   // the group's last piece: its columns are in registers
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float st = __shfl_sync(0xffffffffu, sx[p], i);
-                            if (o < a.O && t0 + c + i < a.T)
-                                il_put(y + (size_t)(c + i) * a.O, fmaf((float)(int)v[i] * sw, st, b));
-                        }
+                    for (int i = 0; i < 16; ++i) {
+                        const float st = __shfl_sync(0xffffffffu, sx0, i);
+                        if (o < a.O && t0 + c + i < a.T)
+                            il_put(y + (size_t)(c + i) * a.O, fmaf((float)(int)v[i] * sw, st, b));
                     }
                 }
                 if (half * 16 >= N) {   // no piece of 16 columns for this group
@@ -261,6 +267,7 @@ int8_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
             } else {
                 // this block's partial sums, [N][128] int32, over the stages (all read)
                 int* part = reinterpret_cast<int*>(smem);
+#pragma unroll 1
                 for (int c = half * 16; c < N; c += 32) {
                     uint32_t v[32];
                     tmem_ld_32x32b_x16(tacc + (uint32_t)c, v);
@@ -284,11 +291,16 @@ int8_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
             const float b = (a.bias != nullptr && o < a.O) ? __ldg(a.bias + o) : 0.f;
             OutT* y = static_cast<OutT*>(a.y) + (size_t)t0 * a.O + o;
             const int c1 = min((N * (rank + 1)) / S, a.T - t0);
+#pragma unroll 1
             for (int c = (N * rank) / S + half; c < c1; c += 2) {
+                const float st = __ldcg(a.sx + t0 + c);
                 const uint32_t off = smem_u32(smem) + (uint32_t)(c * 128 + ch) * 4u;
-                int v = 0;
-                for (int r = 0; r < S; ++r) v += ld_shared_cluster_s32(mapa_shared(off, (uint32_t)r));
-                if (o < a.O) il_put(y + (size_t)c * a.O, fmaf((float)v * sw, a.sx[t0 + c], b));
+                int u[8], v = 0;
+#pragma unroll
+                for (int r = 0; r < 8; ++r) u[r] = r < S ? ld_shared_cluster_s32(mapa_shared(off, (uint32_t)r)) : 0;
+#pragma unroll
+                for (int r = 0; r < 8; ++r) v += u[r];
+                if (o < a.O) il_put(y + (size_t)c * a.O, fmaf((float)v * sw, st, b));
             }
         }
         cluster_barrier_sync();   // no block leaves while its partial sums may be read
@@ -325,6 +337,38 @@ cudaError_t launch_il(const IlArgs& a, const CUtensorMap* maps, int grid, cudaSt
 }
 }  // namespace
 
+// How many clusters of S blocks of these kernels (one block per SM) can be resident at
+// once on the current device; 0 if unknown.  (On a B200 that is 148, 74, 45, 33, 26, 22, 15, 15 for
+// S = 1 .. 8: an SM that is left over in its GPC holds no cluster.)
+int int8_cluster_capacity(int S) {
+    static int cache[64][9];
+    static std::once_flag once[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || S < 1 || S > 8) return 0;
+    std::call_once(once[dev], [dev]() {
+        auto kern = int8_linear_kernel<float>;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess) return;
+        for (int c = 1; c <= 8; ++c) {
+            cudaLaunchAttribute at[1];
+            at[0].id = cudaLaunchAttributeClusterDimension;
+            at[0].val.clusterDim.x = (unsigned)c;
+            at[0].val.clusterDim.y = 1;
+            at[0].val.clusterDim.z = 1;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3((unsigned)c);
+            cfg.blockDim = dim3(kIlThreads);
+            cfg.dynamicSmemBytes = 200 * 1024;
+            cfg.attrs = at;
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&cache[dev][c], kern, &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                cache[dev][c] = 0;
+            }
+        }
+    });
+    return cache[dev][S];
+}
+
 // Tile width and K split.  A tile of N tokens costs about 2 N cycles of MMA for each
 // 128 bytes of K, or the time of its (128 + N) * 128 bytes at about 48 bytes per cycle
 // and SM, and some 1500 cycles of start and epilogue (more where a cluster meets);
@@ -336,9 +380,8 @@ void int8_linear_plan(int T, int K, int O, int sms, int* N_out, int* S_out) {
     *S_out = 1;
     for (int N = 16; N <= 256; N *= 2) {
         const long long tiles = (long long)tiles_o * ((T + N - 1) / N);
-        for (int S = 1; S <= 8; S *= 2) {
-            // (clusters of S do not fill every SM: count them 8/9)
-            if (S > 1 && (N > 64 || tiles * S > (long long)sms * 8 / 9 || KB / S < 2)) continue;
+        for (int S = 1; S <= 8; ++S) {
+            if (S > 1 && (N > 64 || tiles > int8_cluster_capacity(S) || KB / S < 2)) continue;
             const double waves = S > 1 ? 1.0 : (double)((tiles + sms - 1) / sms);
             const double mma = 2.0 * N, load = (128.0 + N) * 128.0 / 48.0;
             const double per = (double)((KB + S - 1) / S) * (mma > load ? mma : load);

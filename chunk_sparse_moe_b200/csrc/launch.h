@@ -146,6 +146,7 @@ struct IlArgs {
     int stages;               // set by the launcher
     unsigned long long wait_ns;
 };
+int int8_cluster_capacity(int S);
 void int8_linear_plan(int T, int K, int O, int sms, int* N, int* S);
 // maps: W [O, K] (box {128, 128}) and q [T, K] (box {128, N}), bytes, 128-byte swizzle
 cudaError_t launch_int8_linear(IlArgs a, const CUtensorMap* maps, bool bf16_out, int sms, cudaStream_t s);
@@ -157,7 +158,7 @@ struct X8Bufs {
     int32_t* counts;          // [E] tokens of each expert
     int32_t* list;            // [E, Tcap] the tokens of each expert, ascending
     int32_t* tpos;            // [E, C32 + 1] how many of them come before token 32 c (last: all)
-    float2* fpair;            // [E, Tcap] gate * scale of h, and gate, of each listed token
+    float4* pair;             // [E, Tcap] of each listed token: its index (bits), gate * scale of h, gate, 0
     int8_t* hq;               // [E * Tcap, d_e] h of each listed token in 8 bits
     int Tcap;
     int C32;                  // ceil(T / 32) of the slice
@@ -178,8 +179,8 @@ struct X8In {
     int stages;               // set by the launcher
     unsigned long long wait_ns;
 };
-// maps: W_in [E * d_e, d_h] (box {128, 128}) and xq [T, d_h] (box {128, 1}: gathered)
-cudaError_t launch_int8_experts_in(X8In a, const CUtensorMap* maps, int sms, cudaStream_t s);
+// map: W_in [E * d_e, d_h] (box {128, 128})
+cudaError_t launch_int8_experts_in(X8In a, const CUtensorMap& map, int sms, cudaStream_t s);
 
 struct X8Out {
     X8Bufs w;
@@ -191,12 +192,12 @@ struct X8Out {
     int KBe;                  // d_e / 128
     int slabs;                // d_h / 128
     int TT;                   // tokens per tile (a multiple of 32)
-    int NB;                   // pairs multiplied at a time (a multiple of 16, at most 64)
+    int NB;                   // pairs multiplied at a time (16, 32 or 64)
     int S;                    // blocks per cluster
     int stages;               // set by the launcher
     unsigned long long wait_ns;
 };
-// maps: W_out [E * d_h, d_e] (box {128, 128}) and hq [E * Tcap, d_e] (box {128, 16})
+// maps: W_out [E * d_h, d_e] (box {128, 128}) and hq [E * Tcap, d_e] (boxes {128, 16 | 32 | 64})
 cudaError_t launch_int8_experts_out(X8Out a, const CUtensorMap* maps, cudaStream_t s);
 
 }  // namespace bffn
