@@ -43,7 +43,13 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
+    """The current device's current stream (as ``torch.cuda.current_stream().cuda_stream``, without
+    building a Stream object: 0.3 us instead of 3 a call)."""
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+
+
+def _empty(rows: int, cols: int, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
 
 
 def version() -> int:
@@ -242,9 +248,9 @@ def route_topk(logits: torch.Tensor, k: int, scores: str = "softmax", bias: Opti
     if bias is not None:
         _want(bias, "bias", torch.float32, (E,), dev)
     if out is None:
-        gates = torch.empty((T, E), dtype=torch.float32, device=dev)
-        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
-        weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+        gates = _empty(T, E, torch.float32, dev)
+        ids = _empty(T, k, torch.int32, dev)
+        weights = _empty(T, k, torch.float32, dev)
     else:
         gates, ids, weights = out
         _want(gates, "gates", torch.float32, (T, E), dev)
@@ -307,7 +313,7 @@ def int8_linear(x: torch.Tensor, W: torch.Tensor, s_w: torch.Tensor, bias: Optio
     if bias is not None:
         _want(bias, "bias", torch.float32, (O,), dev)
     if y is None:
-        y = torch.empty((T, O), dtype=out_dtype or x.dtype, device=dev)
+        y = _empty(T, O, out_dtype or x.dtype, dev)
     else:
         _want(y, "y", out_dtype or y.dtype, (T, O), dev)
     if workspace is None:
@@ -347,7 +353,7 @@ def forward_int8(x: torch.Tensor, gates: torch.Tensor, W_in: torch.Tensor, s_in:
                 _want(t, what, torch.float32, shape, dev)
         opts = ctypes.byref(_lib.LayerOpts(_ptr(b_in), _ptr(b_out), _ptr(ln_weight), _ptr(ln_bias), float(ln_eps)))
     if y is None:
-        y = torch.empty((T, d_h), dtype=x.dtype, device=dev)
+        y = _empty(T, d_h, x.dtype, dev)
     else:
         _want(y, "y", x.dtype, (T, d_h), dev)
     if workspace is None:

@@ -45,7 +45,7 @@ namespace {
 constexpr int kPrepBatch = 16;   // gates a thread has in flight
 
 template <int C>
-__global__ void __launch_bounds__(kQThreads, 3) int8_prepare_kernel(const __nv_bfloat16* __restrict__ x,
+__global__ void __launch_bounds__(kQThreads) int8_prepare_kernel(const __nv_bfloat16* __restrict__ x,
                                                                  const float* __restrict__ gates, int T, int d_h,
                                                                  int E, int W, const X8Bufs w) {
     constexpr int kWarps = kQThreads / 32;
@@ -978,6 +978,7 @@ cudaError_t launch_int8_prepare(const __nv_bfloat16* x, const float* gates, int 
     cudaLaunchConfig_t cfg = x8_config(E + (T + per - 1) / per, kQThreads, 0, s, at, 1);
     if (p.C == 0) return cudaLaunchKernelEx(&cfg, int8_prepare_kernel<0>, x, gates, T, d_h, E, p.W, w);
     if (p.C == 2) return cudaLaunchKernelEx(&cfg, int8_prepare_kernel<2>, x, gates, T, d_h, E, p.W, w);
+    if (p.C == 4) return cudaLaunchKernelEx(&cfg, int8_prepare_kernel<4>, x, gates, T, d_h, E, p.W, w);
     return cudaLaunchKernelEx(&cfg, int8_prepare_kernel<8>, x, gates, T, d_h, E, p.W, w);
 }
 

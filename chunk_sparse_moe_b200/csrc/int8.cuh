@@ -99,11 +99,23 @@ __device__ __forceinline__ float chunk_value(const uint4& u, int i) {
     else return __uint_as_float(w[i]);
 }
 
-// 16 bytes of a row (V values) in 8 bits.  v * inv is rounded by adding 1.5 * 2^23 (the
-// whole number is the sum's low byte); what was rounded off tells whether a value is near
-// the border of two whole numbers, and such a chunk is done again exactly.
+// 16 bytes of a row (V values) in 8 bits, packed.  v * inv is rounded by adding 1.5 * 2^23
+// (the whole number is the sum's low byte); what was rounded off tells whether a value is
+// near the border of two whole numbers, and such a chunk is done again exactly.  bf16
+// values meet the border itself often (one in 256 where amax is a power of two), but
+// 127 v - q amax is exact for them in fp32; fp32 values (one chunk in some hundred)
+// are divided in 64 bits, in a function of its own so that it costs no registers here.
 template <typename T>
-__device__ __forceinline__ void quantize_chunk(const uint4& u, const RowScale& r, int8_t* out) {
+__device__ __noinline__ uint2 quantize_chunk_exact(uint4 u, RowScale r) {
+    constexpr int V = 16 / (int)sizeof(T);
+    uint32_t p[2] = {0u, 0u};
+#pragma unroll 1
+    for (int i = 0; i < V; ++i)
+        p[i >> 2] |= ((uint32_t)quantize_exact(chunk_value<T>(u, i), r) & 255u) << (8 * (i & 3));
+    return make_uint2(p[0], p[1]);
+}
+template <typename T>
+__device__ __forceinline__ uint2 quantize_chunk(const uint4& u, const RowScale& r) {
     constexpr int V = 16 / (int)sizeof(T);
     constexpr float kMagic = 12582912.f;
     uint32_t b[V];
@@ -115,17 +127,28 @@ __device__ __forceinline__ void quantize_chunk(const uint4& u, const RowScale& r
         b[i] = __float_as_uint(t);
         worst = fmaxf(worst, fabsf(fmaf(v, r.inv, kMagic - t)));
     }
-    if (worst > 0.49998f) {   // (inv is off by 2^-24 of itself: the product by 8e-6 at most)
+    // (inv is off by 2^-24 of itself: the product by 8e-6 at most)
+    if (worst > 0.49998f) {
+        if constexpr (sizeof(T) == 4) {
+            return quantize_chunk_exact<T>(u, r);
+        } else {
+            const float down = r.amax > 1.f ? 0.00390625f : 1.f;   // (127 v stays finite, and exact)
+            const float amax = r.amax * down, half = 0.5f * amax;
 #pragma unroll
-        for (int i = 0; i < V; ++i) b[i] = (uint32_t)quantize_exact(chunk_value<T>(u, i), r);
+            for (int i = 0; i < V; ++i) {
+                const float q = __uint_as_float(b[i]) - kMagic;
+                const float d = fmaf(-q, amax, 127.f * (chunk_value<T>(u, i) * down));
+                // past the border, or on it with an odd number: the next one on d's side
+                if (fabsf(d) > half || (fabsf(d) == half && (b[i] & 1u))) b[i] += d > 0.f ? 1u : ~0u;
+            }
+        }
     }
-    uint32_t p[V / 4];
+    uint32_t p[2] = {0u, 0u};
 #pragma unroll
     for (int i = 0; i < V / 4; ++i)
         p[i] = __byte_perm(__byte_perm(b[4 * i], b[4 * i + 1], 0x0040), __byte_perm(b[4 * i + 2], b[4 * i + 3], 0x0040),
                            0x5410);
-    if constexpr (V == 8) *reinterpret_cast<uint2*>(out) = make_uint2(p[0], p[1]);
-    else *reinterpret_cast<uint32_t*>(out) = p[0];
+    return make_uint2(p[0], p[1]);
 }
 
 // W threads (a multiple of 32; thread `t` of them, meeting at named barrier `bar` when
@@ -163,13 +186,9 @@ __device__ __forceinline__ void quantize_row(const T* __restrict__ v, int K, int
         for (int c = 0; c < C; ++c) {
             const int k = (c * W + t) * V;
             if (k < K) {
-                if (r.inv != 0.f) {
-                    quantize_chunk<T>(u[c], r, q + k);
-                } else if constexpr (V == 8) {
-                    *reinterpret_cast<uint2*>(q + k) = make_uint2(0u, 0u);
-                } else {
-                    *reinterpret_cast<uint32_t*>(q + k) = 0u;
-                }
+                const uint2 p = r.inv != 0.f ? quantize_chunk<T>(u[c], r) : make_uint2(0u, 0u);
+                if constexpr (V == 8) *reinterpret_cast<uint2*>(q + k) = p;
+                else *reinterpret_cast<uint32_t*>(q + k) = p.x;
             }
         }
     } else {
@@ -179,7 +198,7 @@ __device__ __forceinline__ void quantize_row(const T* __restrict__ v, int K, int
 
 // How a block of 256 threads rounds rows of K values: W threads a row, C chunks of 16
 // bytes a thread (0: two passes).  Few rows are spread over more threads (what counts
-// is the way through one row), many keep a warp to a row where it fits (no barrier).
+// is the way through one row); many take fewer threads a row, four chunks each.
 constexpr int kQThreads = 256;
 struct QuantPlan {
     int W, C;
@@ -188,7 +207,7 @@ inline QuantPlan quantize_plan(int rows, int K, int elem_bytes) {
     const int V = 16 / elem_bytes;
     QuantPlan p{kQThreads, 0};
     if (K % V != 0 || K / V > 8 * kQThreads) return p;
-    p.C = rows <= 296 && K / V <= 2 * kQThreads ? 2 : 8;
+    p.C = K / V > 4 * kQThreads ? 8 : (rows <= 296 && K / V <= 2 * kQThreads ? 2 : 4);
     p.W = 32;
     while (p.W * p.C < K / V) p.W *= 2;
     return p;

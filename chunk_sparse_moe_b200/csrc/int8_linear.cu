@@ -63,6 +63,7 @@ cudaError_t launch_quantize_t(const T* v, int rows, int K, int8_t* q, float* sca
     cfg.numAttrs = 1;
     if (p.C == 0) return cudaLaunchKernelEx(&cfg, quantize_rows_kernel<T, 0>, v, rows, K, p.W, q, scale);
     if (p.C == 2) return cudaLaunchKernelEx(&cfg, quantize_rows_kernel<T, 2>, v, rows, K, p.W, q, scale);
+    if (p.C == 4) return cudaLaunchKernelEx(&cfg, quantize_rows_kernel<T, 4>, v, rows, K, p.W, q, scale);
     return cudaLaunchKernelEx(&cfg, quantize_rows_kernel<T, 8>, v, rows, K, p.W, q, scale);
 }
 }  // namespace

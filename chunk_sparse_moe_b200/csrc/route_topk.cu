@@ -134,8 +134,13 @@ struct Key64 {
     }
 };
 
-__device__ __forceinline__ float tk_exp(float v) { return expf(v); }
+// Scores for the choice.  In fp32 from the fast exponential and division: off by less than
+// 1e-6 (s <= 1, and the exponent's error of 2^-24 |z| comes in times s (1 - s) or s), a
+// quarter of the gap at which the choice is made again in 64 bits.
+__device__ __forceinline__ float tk_exp(float v) { return __expf(v); }
 __device__ __forceinline__ double tk_exp(double v) { return exp(v); }
+__device__ __forceinline__ float tk_sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+__device__ __forceinline__ double tk_sigmoid(double z) { return 1.0 / (1.0 + exp(-z)); }
 
 template <typename R>
 __device__ __forceinline__ R tk_warp_sum(R v) {
@@ -149,6 +154,7 @@ struct TkArgs {
     int T, E, k;
     int sigmoid;           // scores: 1 sigmoid, 0 softmax
     int n_group, topk_group, per;   // experts per group = E / n_group
+    int lane_groups;       // groups are whole lanes, a power of two of them
     int renorm;
     float scale;
     float* gates;          // [T, E] or nullptr
@@ -165,7 +171,7 @@ __device__ __forceinline__ void tk_choice_keys(const TkArgs& a, const float (&z)
     R s[NJ];
     if (a.sigmoid) {
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) s[j] = R(1) / (R(1) + tk_exp(-(R)z[j]));
+        for (int j = 0; j < NJ; ++j) s[j] = tk_sigmoid((R)z[j]);
     } else {
         R part = R(0);
 #pragma unroll
@@ -186,6 +192,51 @@ __device__ __forceinline__ void tk_choice_keys(const TkArgs& a, const float (&z)
         const R c = s[j] + (R)b;
         key[j] = (z[j] > -INFINITY && c > -INFINITY) ? K::of(c) : typename K::Bits(0);
     }
+}
+
+// tk_keep_groups for groups that are whole lanes, a power of two of them (32 / n_group, as with
+// 32 NJ experts in a power of two of groups): the two largest keys of a group meet in
+// butterflies.  Same result.
+template <int NJ>
+__device__ __forceinline__ bool tk_keep_lane_groups(const TkArgs& a, int lane, uint32_t (&key)[NJ]) {
+    uint32_t b1 = 0, b2 = 0;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+        b2 = max(b2, min(b1, key[j]));
+        b1 = max(b1, key[j]);
+    }
+    const int L = 32 / a.n_group;   // lanes per group
+    for (int o = 1; o < L; o <<= 1) {
+        const uint32_t c1 = __shfl_xor_sync(0xffffffffu, b1, o), c2 = __shfl_xor_sync(0xffffffffu, b2, o);
+        b2 = max(min(b1, c1), max(b2, c2));
+        b1 = max(b1, c1);
+    }
+    // the group's value, in its first lane
+    uint32_t gv = 0;
+    if (b1 != 0 && (lane & (L - 1)) == 0)
+        gv = Key32::of(Key32::value(b1) + (b2 != 0 ? Key32::value(b2) : 0.f));
+    uint32_t kept = 0;   // lanes of the kept groups
+    const uint32_t lanes = L == 32 ? 0xffffffffu : (1u << L) - 1u;
+    float last = 0.f;
+    bool close = false;
+    for (int n = 0; n <= a.topk_group && n < a.n_group; ++n) {
+        const uint32_t m = Key32::warp_max(gv);
+        if (m == 0) break;
+        const float v = Key32::value(m);
+        if (n == a.topk_group) {
+            close = last - v <= 8e-6f * (1.f + fabsf(v));
+            break;
+        }
+        const int src = __ffs(__ballot_sync(0xffffffffu, gv == m)) - 1;
+        if (lane == src) gv = 0;
+        kept |= lanes << src;
+        last = v;
+    }
+    if (!(kept >> lane & 1u)) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) key[j] = 0;
+    }
+    return close;
 }
 
 // Of the groups of `per` neighbouring experts, keep the topk_group of largest
@@ -319,7 +370,14 @@ __device__ __forceinline__ bool tk_choose(const TkArgs& a, const float (&z)[NJ],
     bool close = false;
     if (scored) {
         tk_choice_keys<NJ, K>(a, z, a.bias, lane, key, m, sum);
-        if (a.n_group > 1) close = tk_keep_groups<NJ, K>(a, lane, key, static_cast<typename K::Bits*>(srow));
+        if (a.n_group > 1) {
+            if constexpr (sizeof(typename K::Bits) == 4) {
+                if (a.lane_groups) close = tk_keep_lane_groups<NJ>(a, lane, key);
+                else close = tk_keep_groups<NJ, K>(a, lane, key, static_cast<typename K::Bits*>(srow));
+            } else {
+                close = tk_keep_groups<NJ, K>(a, lane, key, static_cast<typename K::Bits*>(srow));
+            }
+        }
     } else {
 #pragma unroll
         for (int j = 0; j < NJ; ++j) key[j] = z[j] > -INFINITY ? K::of(z[j]) : typename K::Bits(0);
@@ -560,6 +618,7 @@ cudaError_t launch_route_topk(const void* logits, bool bf16, const float* bias, 
     a.n_group = topk_group == n_group ? 1 : n_group;   // every group kept: no groups
     a.topk_group = topk_group;
     a.per = E / n_group;
+    a.lane_groups = E % 32 == 0 && n_group <= 32 && (n_group & (n_group - 1)) == 0;
     a.renorm = renorm;
     a.scale = scale;
     a.gates = gates;

@@ -58,6 +58,21 @@ def test_quantize_borders_and_extremes():
     assert torch.isnan(s[4:]).all() and not q[4:].any()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("top", [3e38, 4.0, 1.0, 3.75, 2.0 ** -119, 2.0 ** -60])
+def test_quantize_ranges(top, dtype):
+    """Rows from the largest values to the smallest, many of them halves between two whole numbers."""
+    bffn = require_cuda()
+    rng = np.random.default_rng(7)
+    w = torch.from_numpy((rng.integers(-256, 257, (8, 2048)) / 256).astype(np.float32))
+    w[:, 0] = 1.0
+    w = (w.double() * top).to(dtype)
+    q, s = bffn.quantize_int8(w.cuda())
+    rq, rs = quantized(w.double().numpy())
+    assert np.array_equal(q.cpu().numpy().astype(np.int64), rq)
+    assert np.all(np.abs(s.double().cpu().numpy() - rs) <= U * rs + 2.0 ** -150)
+
+
 def check(bffn, x, W, s_w, bias, out_dtype, **kw):
     d = lambda t: None if t is None else t.cuda()
     y = bffn.int8_linear(d(x), d(W), d(s_w), bias=d(bias), out_dtype=out_dtype, **kw)
