@@ -570,10 +570,11 @@ blockffn_status blockffn_forward_int8(const void* x, const float* gates, const i
         in.s_in = s_in;
         in.b_in = b_in;
         in.ctl = ctl;
+        in.T = n;
         in.E = E;
         in.d_e = d_e;
         in.KB = d_h / 128;
-        in.N = n <= 16 ? 16 : n <= 32 ? 32 : (n <= 1024 || MT > 2) ? 64 : 128;
+        in.lgN = n <= 16 ? 4 : n <= 32 ? 5 : (n <= 1024 || MT > 2) ? 6 : 7;
         in.CS = n <= 128 ? 4 : n <= 1024 ? 2 : 1;
         in.stages = 0;
         in.wait_ns = g_wait_ns.load();
@@ -589,23 +590,24 @@ blockffn_status blockffn_forward_int8(const void* x, const float* gates, const i
         out.KBe = MT;
         out.slabs = d_h / 128;
         out.TT = n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256;
-        out.NB = n <= 16 ? 16 : n <= 32 ? 32 : 64;
+        out.lgNB = n <= 16 ? 4 : n <= 32 ? 5 : 6;
         out.S = 1;
         const long long items = (long long)out.slabs * ((n + out.TT - 1) / out.TT);
         for (int S = 2; S <= 8; ++S)
             if (items <= int8_cluster_capacity(S) && S <= E) out.S = S;
         out.stages = 0;
         out.wait_ns = in.wait_ns;
-        CUtensorMap maps[5];
+        CUtensorMap maps[6];
         if (!make_map_u8(&maps[0], W_in, (uint64_t)d_h, (uint64_t)E * d_e, 128) ||
-            !make_map_u8(&maps[1], W_out, (uint64_t)d_e, (uint64_t)E * d_h, 128) ||
-            !make_map_u8(&maps[2], w.hq, (uint64_t)d_e, (uint64_t)E * L.Tcap, 16) ||
-            !make_map_u8(&maps[3], w.hq, (uint64_t)d_e, (uint64_t)E * L.Tcap, 32) ||
-            !make_map_u8(&maps[4], w.hq, (uint64_t)d_e, (uint64_t)E * L.Tcap, 64))
+            !make_map_u8(&maps[1], w.xq, (uint64_t)d_h, (uint64_t)n, 1u << in.lgN) ||
+            !make_map_u8(&maps[2], W_out, (uint64_t)d_e, (uint64_t)E * d_h, 128) ||
+            !make_map_u8(&maps[3], w.hq, (uint64_t)d_e, (uint64_t)E * L.Tcap, 16) ||
+            !make_map_u8(&maps[4], w.hq, (uint64_t)d_e, (uint64_t)E * L.Tcap, 32) ||
+            !make_map_u8(&maps[5], w.hq, (uint64_t)d_e, (uint64_t)E * L.Tcap, 64))
             return fail(BLOCKFFN_ERR_CUDA, "cuTensorMapEncodeTiled failed");
-        e = launch_int8_experts_in(in, maps[0], G, s);
+        e = launch_int8_experts_in(in, maps, G, s);
         if (e != cudaSuccess) return cuda_fail(e, "8-bit experts-in launch");
-        e = launch_int8_experts_out(out, maps + 1, s);
+        e = launch_int8_experts_out(out, maps + 2, s);
         if (e != cudaSuccess) return cuda_fail(e, "8-bit experts-out launch");
     }
     if (ln_w) {
@@ -775,7 +777,7 @@ blockffn_status blockffn_forward(const void* x, const float* gates, const void* 
         e = launch_expert_bias_sum(g, t_counts, t_idx, t_tmask, ctl, b_out, T, d_h, E, n, ybias, s);
         if (e != cudaSuccess) return cuda_fail(e, "expert bias launch");
     }
-    CUtensorMap maps[5];
+    CUtensorMap maps[6];
     // expert-out partial tiles [blocks][2 slots][N/4 token quads][128 rows x 4 tokens]
     // fp32, seen as lines of 512 floats; a box is 32 rows of every token quad
     if (!make_map(&maps[0], x, (uint64_t)d_h, (uint64_t)T, (uint32_t)L.N) ||

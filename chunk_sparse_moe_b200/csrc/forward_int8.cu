@@ -17,7 +17,8 @@
 //
 //   prepare    : the tokens' 8-bit rows; per expert the ascending list of its tokens
 //                and, at every 32nd token, how many came before
-//   experts_in : tiles of one expert x up to N of its tokens, all of d_e; x rows are
+//   experts_in : tiles of one expert x up to N of its tokens, all of d_e.  Up to 64 tokens
+//                are all multiplied (what counts is the weights' bytes); else x rows are
 //                gathered in 16-byte asynchronous copies straight into the MMA's
 //                swizzled layout (two warps; TMA's gather of four rows an operation took
 //                about 60 cycles each, 18 us for a tile of 128 rows at d_h 2048).  The tile holds whole rows of h, so the epilogue finds
@@ -47,17 +48,17 @@ constexpr int kPrepBatch = 16;   // gates a thread has in flight
 template <int C>
 __global__ void __launch_bounds__(kQThreads) int8_prepare_kernel(const __nv_bfloat16* __restrict__ x,
                                                                  const float* __restrict__ gates, int T, int d_h,
-                                                                 int E, int W, const X8Bufs w) {
+                                                                 int E, int lgW, const X8Bufs w) {
     constexpr int kWarps = kQThreads / 32;
     __shared__ uint32_t red[kPrepBatch * kWarps + 1];
     griddep_wait();
     griddep_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if ((int)blockIdx.x >= E) {
-        const int g = tid / W, t = ((int)blockIdx.x - E) * (kQThreads / W) + g;
+        const int W = 1 << lgW, g = tid >> lgW, t = (((int)blockIdx.x - E) << (8 - lgW)) + g;
         if (t < T)
-            quantize_row<__nv_bfloat16, C>(x + (size_t)t * d_h, d_h, w.xq + (size_t)t * d_h, w.sx + t, W, tid - g * W,
-                                           1 + g, red + g * (W / 32));
+            quantize_row<__nv_bfloat16, C>(x + (size_t)t * d_h, d_h, w.xq + (size_t)t * d_h, w.sx + t, W, tid & (W - 1),
+                                           1 + g, red + (g << lgW >> 5));
         return;
     }
     const int e = blockIdx.x;
@@ -181,12 +182,13 @@ __device__ __forceinline__ void tmem_ld_piece(uint32_t taddr, int (&v)[8]) {
     for (int j = 0; j < 8; ++j) v[j] = (int)u[j];
 }
 
-// What the epilogue does with n <= PW columns (tokens) of int32 sums: h, its scale over
-// all of d_e (the four warps of the group meet in colmax), 8-bit h and the pair's factors.
-// Lane i (of PW) holds column i's token, its scale and gate.
+// What the epilogue does with PW columns (tokens) of int32 sums: h, its scale over all of
+// d_e (the four warps of the group meet in colmax), 8-bit h and the pair's factors.  Lane i
+// (of PW) holds column i's token, its scale and gate, and the place of the pair in the
+// expert's list (slot, -1: no pair); pair0: the list's first pair.
 template <int MT, int PW>
-__device__ __forceinline__ void xi_finish(const X8In& a, XiShared& sh, const int (&v)[MT][PW], int n,
-                                          size_t pair0, int token, float sx, float gate, const float (&si)[MT],
+__device__ __forceinline__ void xi_finish(const X8In& a, XiShared& sh, const int (&v)[MT][PW], size_t pair0, int slot,
+                                          int token, float sx, float gate, const float (&si)[MT],
                                           const float (&bi)[MT], int group, int q, int lane, uint32_t& parity) {
     float h[MT][PW];
     uint32_t mine = 0;
@@ -209,15 +211,16 @@ __device__ __forceinline__ void xi_finish(const X8In& a, XiShared& sh, const int
     named_bar_sync(1 + group, 128);
     RowScale r = {0.f, 0.f, 0.f};
     if (lane < PW) r = row_scale(max(max(cm[0][lane], cm[1][lane]), max(cm[2][lane], cm[3][lane])));
-    if (q == 0 && lane < n)
-        a.w.pair[pair0 + lane] = make_float4(__int_as_float(token), gate * r.scale, gate, 0.f);
+    if (q == 0 && lane < PW && slot >= 0)
+        a.w.pair[pair0 + slot] = make_float4(__int_as_float(token), gate * r.scale, gate, 0.f);
     int8_t* out = a.w.hq + pair0 * a.d_e + q * 32 + lane;
 #pragma unroll
     for (int i = 0; i < PW; ++i) {
         const float inv = __shfl_sync(0xffffffffu, r.inv, i);
-        if (i < n) {
+        const int at = __shfl_sync(0xffffffffu, slot, i);
+        if (at >= 0) {
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) out[(size_t)i * a.d_e + mt * 128] = (int8_t)(int)rintf(h[mt][i] * inv);
+            for (int mt = 0; mt < MT; ++mt) out[(size_t)at * a.d_e + mt * 128] = (int8_t)(int)rintf(h[mt][i] * inv);
         }
     }
 }
@@ -226,25 +229,25 @@ __device__ __forceinline__ void xi_finish(const X8In& a, XiShared& sh, const int
 
 template <int MT>
 __global__ void __launch_bounds__(kXiThreads, 1)
-int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const X8In a) {
+int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                       const X8In a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     // Columns the epilogue holds at a time.  (Small pieces in rolled loops: at a decode step every
     // instruction of the epilogue runs once, from a cold instruction cache.)
     constexpr int PW = 8, PWX = 4;
-    const int N = a.N;
+    const int N = 1 << a.lgN;
     const int a_bytes = MT * kXTile, stage_bytes = a_bytes + N * 128;
     XiShared& sh = *reinterpret_cast<XiShared*>(smem + (size_t)a.stages * stage_bytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int crank = a.CS > 1 ? (int)cluster_ctarank() : 0;
-    const int cluster = (int)blockIdx.x / a.CS;
     uint32_t cols = 32;
     while ((int)cols < 2 * MT * N) cols *= 2;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < a.stages; ++i) {
             mbar_init(&sh.full[i], 1);
-            mbar_init(&sh.gathered[i], kXGather);
+            mbar_init(&sh.gathered[i], a.T <= N ? 1 : kXGather);
             mbar_init(&sh.empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -255,6 +258,7 @@ int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const X8In a) {
         fence_mbar_init();
         sh.abort = 0;
         prefetch_tmap(&tm_w);
+        prefetch_tmap(&tm_x);
     }
     if (warp == 1) {
         tmem_alloc(&sh.tmem_base, cols);
@@ -272,7 +276,7 @@ int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const X8In a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             if (32 * i >= a.E) break;
-            const int e = 32 * i + lane, nt = (cnt[i] + N - 1) / N;
+            const int e = 32 * i + lane, nt = (cnt[i] + N - 1) >> a.lgN;
             int inc = nt;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -281,7 +285,8 @@ int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const X8In a) {
             }
             if (e < a.E) {
                 sh.cnt[e] = cnt[i];
-                sh.per[e] = nt > 0 ? ((cnt[i] + nt - 1) / nt + 15) & ~15 : 0;
+                // (at most 8192 tokens: the quotient by way of fp32 is exact, and quicker)
+                sh.per[e] = nt > 0 ? ((int)__fdividef((float)(cnt[i] + nt) - 0.5f, (float)nt) + 15) & ~15 : 0;
                 sh.first[e] = run + inc - nt;
             }
             run += __shfl_sync(0xffffffffu, inc, 31);
@@ -298,13 +303,16 @@ int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const X8In a) {
     const uint64_t limit = a.wait_ns;
     const int all = sh.first[a.E], tiles = sh.abort ? 0 : all;
 
-    // S blocks per tile: as many as fill the grid once (a power of two, at most the cluster)
-    int S = 1;
-    while (2 * S <= a.CS && all * 2 * S <= (int)gridDim.x && a.KB >= 4 * S) S *= 2;
-    const int sub = crank % S;
-    const int first = (cluster * a.CS + crank) / S;
-    const int step = (int)gridDim.x / S;
-    const int kb0 = a.KB * sub / S, kb1 = a.KB * (sub + 1) / S;
+    // A slice of at most N tokens is not gathered: column c of every tile is token c, all
+    // of them are multiplied, and the epilogue takes the columns of the expert's tokens.
+    const bool dense = a.T <= N;
+
+    // S = 2^lgS blocks per tile: as many as fill the grid once, at most the cluster
+    int lgS = 0;
+    while ((2 << lgS) <= a.CS && (all << (lgS + 1)) <= (int)gridDim.x && a.KB >= (4 << lgS)) ++lgS;
+    const int S = 1 << lgS, sub = crank & (S - 1);
+    const int first = (int)blockIdx.x >> lgS, step = (int)gridDim.x >> lgS;
+    const int kb0 = a.KB * sub >> lgS, kb1 = a.KB * (sub + 1) >> lgS;
 
     if (warp == 0) {
         const uint64_t pol = policy_evict_normal();
@@ -341,6 +349,32 @@ int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const X8In a) {
         }
         __syncwarp();
     } else if (warp == 2 || warp == 3 || warp >= 12) {
+        if (dense) {
+            if (warp == 2 && lane == 0) {
+                const uint64_t pol = policy_evict_normal();
+                int st = 0, issued = 0;
+                uint32_t ph = 0;
+                bool ok = true;
+                for (int i = first; i < tiles && ok; i += step) {
+                    for (int kb = kb0; kb < kb1; ++kb) {
+                        ok = wait_bar(&sh.empty[st], ph ^ 1u, limit, &sh.abort, a.ctl, kWaitEmpty);
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(&sh.gathered[st], (uint32_t)(N * 128));
+                        tma_load_2d(smem + (size_t)st * stage_bytes + a_bytes, &tm_x, &sh.gathered[st], kb * 128, 0, pol);
+                        ++issued;
+                        if (++st == a.stages) {
+                            st = 0;
+                            ph ^= 1u;
+                        }
+                    }
+                }
+                const int in_ring = min(issued, a.stages);
+                for (int i = 0; i < in_ring; ++i) {
+                    st = st == 0 ? a.stages - 1 : st - 1;
+                    wait_bar_drain(&sh.gathered[st], (uint32_t)(((issued - 1 - i) / a.stages) & 1), limit, a.ctl);
+                }
+            }
+        } else {
         // Gather: eight lanes copy one token row's 128 bytes in 16-byte pieces into the
         // swizzled layout (piece c of row r lies at c ^ (r & 7)); the warps take four rows
         // each in turn.  The MMA reads the rows through the async proxy, and the fence
@@ -397,6 +431,7 @@ int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const X8In a) {
             }
         }
         cp_async_wait_all();   // (after a timeout: no copy is in flight when the block ends)
+        }
         __syncwarp();
     } else if (warp == 1) {
         const uint64_t desc0 = sw128_kmajor_desc(smem_u32(smem));
@@ -405,7 +440,7 @@ int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const X8In a) {
         bool ok = true;
         for (int i = first; i < tiles && ok; i += step) {
             const XiItem it = xi_item(sh, a.E, i);
-            const uint32_t idesc = idesc_i8_s32(128, (it.rows + 15) & ~15);
+            const uint32_t idesc = idesc_i8_s32(128, ((dense ? a.T : it.rows) + 15) & ~15);
             ok = wait_bar_warp(&sh.acc_empty[buf], bph ^ 1u, limit, &sh.abort, a.ctl, kWaitAccEmpty);
             if (!ok) break;
             tc_fence_after();
@@ -448,51 +483,71 @@ int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const X8In a) {
         uint32_t bph = 0, parity = 0;
         for (int i = first; i < tiles; i += step) {
             const XiItem it = xi_item(sh, a.E, i);
-            const size_t pair = (size_t)it.e * a.w.Tcap + it.base;
+            const size_t pair0 = (size_t)it.e * a.w.Tcap;
+            const int width = dense ? a.T : it.rows;   // columns of the tile
             float si[MT], bi[MT];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
                 si[mt] = __ldg(a.s_in + (size_t)it.e * a.d_e + mt * 128 + ch);
                 bi[mt] = a.b_in != nullptr ? __ldg(a.b_in + (size_t)it.e * a.d_e + mt * 128 + ch) : 0.f;
             }
+            // (dense) the expert's tokens as bits: N <= 128, a register for each 32
+            uint32_t on[4] = {0u, 0u, 0u, 0u};
+            if (dense && S == 1) {
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const int t = 32 * w + lane;
+                    on[w] = __ballot_sync(0xffffffffu, t < a.T && __ldg(a.gates + (size_t)t * a.E + it.e) != 0.f);
+                }
+            }
             // (the group leaves its loop together)
             if (!bar_all(1 + group, wait_bar_warp(&sh.acc_full[buf], bph, limit, &sh.abort, a.ctl, kWaitAccFull))) break;
             tc_fence_after();
             const uint32_t tacc = tmem + (uint32_t)(buf * MT * N) + ((uint32_t)(q * 32) << 16);
             if (S == 1) {
-                if (group * PW >= it.rows && lane == 0) mbar_arrive(&sh.acc_empty[buf]);   // nothing for this group
-                int tk = 0;
+                if (group * PW >= width && lane == 0) mbar_arrive(&sh.acc_empty[buf]);   // nothing for this group
+                int tk = 0, slot = -1;
                 float sx = 0.f, gt = 0.f;
                 auto column = [&](int c) {   // what lane i (of PW) knows of column c + i
                     c += lane & (PW - 1);
-                    if (c >= it.rows) return;
-                    tk = __ldcg(a.w.list + pair + c);
+                    slot = -1;
+                    if (c >= width) return;
+                    if (!dense) {
+                        slot = it.base + c;
+                        tk = __ldcg(a.w.list + pair0 + slot);
+                    } else {
+                        const int w = c >> 5;
+                        const uint32_t word = w == 0 ? on[0] : w == 1 ? on[1] : w == 2 ? on[2] : on[3];
+                        if (!(word >> (c & 31) & 1u)) return;
+                        tk = c;
+                        slot = __popc(word & ((1u << (c & 31)) - 1u)) + (w > 0 ? __popc(on[0]) : 0) +
+                               (w > 1 ? __popc(on[1]) : 0) + (w > 2 ? __popc(on[2]) : 0);
+                    }
                     sx = __ldcg(a.w.sx + tk);
                     gt = __ldg(a.gates + (size_t)tk * a.E + it.e);
                 };
                 column(group * PW);
 #pragma unroll 1
-                for (int c = group * PW; c < it.rows; c += 2 * PW) {
+                for (int c = group * PW; c < width; c += 2 * PW) {
                     int v[MT][PW];
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) tmem_ld_piece(tacc + (uint32_t)(mt * N + c), v[mt]);
-                    const int tk0 = tk;
+                    const int tk0 = tk, slot0 = slot;
                     const float sx0 = sx, gt0 = gt;
                     column(c + 2 * PW);
                     tmem_ld_wait();
-                    if (c + 2 * PW >= it.rows) {   // the group's last piece is in registers
+                    if (c + 2 * PW >= width) {   // the group's last piece is in registers
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);
                     }
-                    xi_finish<MT, PW>(a, sh, v, min(PW, it.rows - c), pair + c, tk0, sx0, gt0, si, bi, group, q, lane,
-                                      parity);
+                    xi_finish<MT, PW>(a, sh, v, pair0, slot0, tk0, sx0, gt0, si, bi, group, q, lane, parity);
                 }
             } else {
                 // partial sums [column][MT * 128] int32 over the stages (all read)
                 int* part = reinterpret_cast<int*>(smem);
 #pragma unroll 1
-                for (int c = group * PW; c < it.rows; c += 2 * PW) {
+                for (int c = group * PW; c < width; c += 2 * PW) {
                     int v[MT][PW];
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) tmem_ld_piece(tacc + (uint32_t)(mt * N + c), v[mt]);
@@ -501,7 +556,7 @@ int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const X8In a) {
                     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                         for (int j = 0; j < PW; ++j)
-                            if (c + j < it.rows) part[((c + j) * MT + mt) * 128 + ch] = v[mt][j];
+                            if (c + j < width) part[((c + j) * MT + mt) * 128 + ch] = v[mt][j];
                 }
             }
             buf ^= 1;
@@ -513,55 +568,64 @@ int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const X8In a) {
         const int q = warp & 3, group = (warp - 4) >> 2, ch = q * 32 + lane;
         float si[MT], bi[MT], sx = 0.f, gt = 0.f;
         int c0 = 0, n = 0, tk = 0;
-        size_t pair = 0;
+        size_t pair0 = 0;
         if (warp >= 4 && warp < 12 && first < tiles) {
-            // this block's columns, half of them for each warp group (at most 16)
+            // this block's share of the listed tokens, half of them for each warp group (at
+            // most 16: N <= 64 where clusters have more than one block)
             const XiItem it = xi_item(sh, a.E, first);
-            const int per = N / S, half = (per + 1) / 2;
+            const int per = (it.rows + S - 1) >> lgS, half = (per + 1) >> 1;
             c0 = sub * per + group * half;
-            n = max(0, min(group == 0 ? c0 + half : (sub + 1) * per, it.rows) - c0);
-            pair = (size_t)it.e * a.w.Tcap + it.base + c0;
+            n = max(0, min(min(c0 + half, (sub + 1) * per), it.rows) - c0);
+            c0 += it.base;
+            pair0 = (size_t)it.e * a.w.Tcap;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
                 si[mt] = __ldg(a.s_in + (size_t)it.e * a.d_e + mt * 128 + ch);
                 bi[mt] = a.b_in != nullptr ? __ldg(a.b_in + (size_t)it.e * a.d_e + mt * 128 + ch) : 0.f;
             }
             if ((lane & 15) < n) {
-                tk = __ldcg(a.w.list + pair + (lane & 15));
+                tk = __ldcg(a.w.list + pair0 + c0 + (lane & 15));
                 sx = __ldcg(a.w.sx + tk);
                 gt = __ldg(a.gates + (size_t)tk * a.E + it.e);
             }
+            // (the tile's column of this lane's token)
+            c0 -= it.base;
         }
+        const int col = dense ? tk : c0 + (lane & 15);
         cluster_barrier_sync();
         if (n > 0 && sh.abort == 0) {
             uint32_t parity = 0;
-            const uint32_t off = smem_u32(smem) + (uint32_t)(c0 * MT * 128 + ch) * 4u;
+            const int base = xi_item(sh, a.E, first).base;
+            const uint32_t off = smem_u32(smem) + (uint32_t)ch * 4u;
 #pragma unroll 1
             for (int b = 0; b < n; b += PWX) {
+                // lane i of the piece: pair b + i, held by lane b + i
+                const int from = (b + lane) & 15;
+                const int slot = lane < PWX && b + lane < n ? base + c0 + b + lane : -1;
                 // (at most four blocks share a tile; all their partial sums in flight at once)
                 int u[4][MT][PWX], v[MT][PWX];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const uint32_t rp = mapa_shared(off, (uint32_t)(crank - sub + (r < S ? r : 0)));
+                for (int j = 0; j < PWX; ++j) {
+                    const int cj = __shfl_sync(0xffffffffu, col, (b + j) & 15);
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
+                    for (int r = 0; r < 4; ++r)
 #pragma unroll
-                        for (int j = 0; j < PWX; ++j)
+                        for (int mt = 0; mt < MT; ++mt)
                             u[r][mt][j] = r < S && b + j < n
-                                              ? ld_shared_cluster_s32(rp + (uint32_t)(((b + j) * MT + mt) * 512)) : 0;
+                                              ? ld_shared_cluster_s32(mapa_shared(off + (uint32_t)((cj * MT + mt) * 512),
+                                                                                  (uint32_t)(crank - sub + r)))
+                                              : 0;
                 }
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                     for (int j = 0; j < PWX; ++j) v[mt][j] = u[0][mt][j] + u[1][mt][j] + u[2][mt][j] + u[3][mt][j];
-                // (lane i of the piece: column b + i, held by lane b + i)
-                const int from = (b + lane) & 15;
-                xi_finish<MT, PWX>(a, sh, v, min(PWX, n - b), pair + b, __shfl_sync(0xffffffffu, tk, from),
-                                  __shfl_sync(0xffffffffu, sx, from), __shfl_sync(0xffffffffu, gt, from), si, bi, group,
-                                  q, lane, parity);
+                xi_finish<MT, PWX>(a, sh, v, pair0, slot, __shfl_sync(0xffffffffu, tk, from),
+                                   __shfl_sync(0xffffffffu, sx, from), __shfl_sync(0xffffffffu, gt, from), si, bi, group,
+                                   q, lane, parity);
             }
         }
-        cluster_barrier_sync();   // no block leaves while its partial sums may be read
+        cluster_barrier_sync_relaxed();   // no block leaves while its partial sums may be read
     }
     tc_fence_before();
     __syncthreads();
@@ -635,13 +699,13 @@ int8_experts_out_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_c
                         const X8Out a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    const int NB = a.NB, TT = a.TT, S = a.S;
-    const int stage_bytes = kXTile + NB * 128;
+    const int NB = 1 << a.lgNB, TT = a.TT, S = a.S;
+    const int stage_bytes = kXTile + (128 << a.lgNB);
     float* acc = reinterpret_cast<float*>(smem + (size_t)a.stages * stage_bytes);   // [TT + 1][128]
     XoShared& sh = *reinterpret_cast<XoShared*>(reinterpret_cast<uint8_t*>(acc) + (size_t)(TT + 1) * 512);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = S > 1 ? (int)cluster_ctarank() : 0;
-    const int item = (int)blockIdx.x / S, slab = item % a.slabs, t0 = item / a.slabs * TT;
+    const int slab = S > 1 ? (int)cluster_id_x() : (int)blockIdx.x, t0 = (int)blockIdx.y * TT;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < a.stages; ++i) {
@@ -686,7 +750,7 @@ int8_experts_out_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_c
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             if (32 * i >= a.E) break;
-            const int ne = (hi[i] - lo[i] + NB - 1) / NB;
+            const int ne = (hi[i] - lo[i] + NB - 1) >> a.lgNB;
             int inc = ne;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -711,7 +775,10 @@ int8_experts_out_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_c
     const uint32_t tmem = sh.tmem_base;
     const uint64_t limit = a.wait_ns;
     const int ents = sh.abort ? 0 : sh.n_ent;
-    const int m0 = ents * rank / S, m1 = ents * (rank + 1) / S;
+    // this block's share (at most 1024 entries: fp32 quotients are exact)
+    const float per_rank = __fdividef(1.f, (float)S);
+    const int m0 = (int)(((float)(ents * rank) + 0.25f) * per_rank);
+    const int m1 = (int)(((float)(ents * (rank + 1)) + 0.25f) * per_rank);
 
     if (warp == 0 || warp == 2) {
         // Warp 0 loads weight tiles, warp 2 the pairs' rows of h: one thread issues a TMA
@@ -904,33 +971,34 @@ int8_experts_out_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_c
     if (S > 1) cluster_barrier_sync();
     else __syncthreads();
     if (sh.abort == 0) {
-        const int ra = TT * rank / S, rb = min(TT * (rank + 1) / S, a.T - t0);
-        for (int i = ra * 16 + (int)threadIdx.x; i < rb * 16; i += kXoThreads) {
-            float f[8];
-            const float* p = acc + i * 8;
-            if (S == 1) {
-                const float4 u = *reinterpret_cast<const float4*>(p), v = *reinterpret_cast<const float4*>(p + 4);
-                f[0] = u.x; f[1] = u.y; f[2] = u.z; f[3] = u.w;
-                f[4] = v.x; f[5] = v.y; f[6] = v.z; f[7] = v.w;
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) f[k] = 0.f;
+        // (a thread four channels of a row)
+        const int ra = (int)(((float)(TT * rank) + 0.25f) * per_rank);
+        const int rb = min((int)(((float)(TT * (rank + 1)) + 0.25f) * per_rank), a.T - t0);
+#pragma unroll 1
+        for (int i = ra * 32 + (int)threadIdx.x; i < rb * 32; i += kXoThreads) {
+            const float* p = acc + i * 4;
+            float4 f = *reinterpret_cast<const float4*>(p);
+            if (S > 1) {
+                float4 u[8];   // all ranks' rows in flight at once
                 const uint32_t off = smem_u32(p);
-                for (int r = 0; r < S; ++r) {
-                    const uint32_t rp = mapa_shared(off, (uint32_t)r);
-                    const float4 u = ld_shared_cluster_f4(rp), v = ld_shared_cluster_f4(rp + 16);
-                    f[0] += u.x; f[1] += u.y; f[2] += u.z; f[3] += u.w;
-                    f[4] += v.x; f[5] += v.y; f[6] += v.z; f[7] += v.w;
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    u[r] = r < S ? ld_shared_cluster_f4(mapa_shared(off, (uint32_t)r)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                f = u[0];
+#pragma unroll
+                for (int r = 1; r < 8; ++r) {
+                    f.x += u[r].x;
+                    f.y += u[r].y;
+                    f.z += u[r].z;
+                    f.w += u[r].w;
                 }
             }
-            __nv_bfloat162 b[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) b[k] = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
-            *reinterpret_cast<uint4*>(a.y + (size_t)(t0 + (i >> 4)) * a.d_h + slab * 128 + (i & 15) * 8) =
-                *reinterpret_cast<const uint4*>(b);
+            const __nv_bfloat162 b0 = __floats2bfloat162_rn(f.x, f.y), b1 = __floats2bfloat162_rn(f.z, f.w);
+            *reinterpret_cast<uint2*>(a.y + (size_t)(t0 + (i >> 5)) * a.d_h + slab * 128 + (i & 31) * 4) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&b0), *reinterpret_cast<const uint32_t*>(&b1));
         }
     }
-    if (S > 1) cluster_barrier_sync();   // no block leaves while its rows may be read
+    if (S > 1) cluster_barrier_sync_relaxed();   // no block leaves while its rows may be read
     tc_fence_before();
     __syncthreads();
     if (warp == 2) tmem_dealloc(tmem, kXoTmem);
@@ -959,13 +1027,13 @@ cudaLaunchConfig_t x8_config(int grid, int threads, size_t smem, cudaStream_t s,
 constexpr int kMaxSmem = 227 * 1024;
 
 template <int MT>
-cudaError_t launch_in(const X8In& a, const CUtensorMap& map, int grid, size_t smem, cudaStream_t s) {
+cudaError_t launch_in(const X8In& a, const CUtensorMap* maps, int grid, size_t smem, cudaStream_t s) {
     auto kern = int8_experts_in_kernel<MT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute at[2];
     cudaLaunchConfig_t cfg = x8_config(grid, kXiThreads, smem, s, at, a.CS);
-    return cudaLaunchKernelEx(&cfg, kern, map, a);
+    return cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], a);
 }
 
 }  // namespace
@@ -973,35 +1041,35 @@ cudaError_t launch_in(const X8In& a, const CUtensorMap& map, int grid, size_t sm
 cudaError_t launch_int8_prepare(const __nv_bfloat16* x, const float* gates, int T, int d_h, int E, const X8Bufs& w,
                                 cudaStream_t s) {
     const QuantPlan p = quantize_plan(T, d_h, 2);
-    const int per = kQThreads / p.W;
+    const int per = kQThreads >> p.lgW;
     cudaLaunchAttribute at[2];
     cudaLaunchConfig_t cfg = x8_config(E + (T + per - 1) / per, kQThreads, 0, s, at, 1);
-    if (p.C == 0) return cudaLaunchKernelEx(&cfg, int8_prepare_kernel<0>, x, gates, T, d_h, E, p.W, w);
-    if (p.C == 2) return cudaLaunchKernelEx(&cfg, int8_prepare_kernel<2>, x, gates, T, d_h, E, p.W, w);
-    if (p.C == 4) return cudaLaunchKernelEx(&cfg, int8_prepare_kernel<4>, x, gates, T, d_h, E, p.W, w);
-    return cudaLaunchKernelEx(&cfg, int8_prepare_kernel<8>, x, gates, T, d_h, E, p.W, w);
+    if (p.C == 0) return cudaLaunchKernelEx(&cfg, int8_prepare_kernel<0>, x, gates, T, d_h, E, p.lgW, w);
+    if (p.C == 2) return cudaLaunchKernelEx(&cfg, int8_prepare_kernel<2>, x, gates, T, d_h, E, p.lgW, w);
+    if (p.C == 4) return cudaLaunchKernelEx(&cfg, int8_prepare_kernel<4>, x, gates, T, d_h, E, p.lgW, w);
+    return cudaLaunchKernelEx(&cfg, int8_prepare_kernel<8>, x, gates, T, d_h, E, p.lgW, w);
 }
 
 // Tokens per tile and blocks per cluster.  A tile of all an expert's tokens reads its
 // weight once, so N grows with T, up to what two accumulators of all d_e rows leave of
 // TMEM (2 * d_e / 128 * N <= 512 columns).  Where
 // the tiles may be fewer than the SMs, clusters let several blocks share a tile.
-cudaError_t launch_int8_experts_in(X8In a, const CUtensorMap& map, int sms, cudaStream_t s) {
-    const int MT = a.d_e / 128, stage = MT * kXTile + a.N * 128;
+cudaError_t launch_int8_experts_in(X8In a, const CUtensorMap* maps, int sms, cudaStream_t s) {
+    const int MT = a.d_e / 128, stage = MT * kXTile + (128 << a.lgN);
     a.stages = kXRing / stage < kXMaxStages ? kXRing / stage : kXMaxStages;
     const size_t smem = 1024 + (size_t)a.stages * stage + sizeof(XiShared);
     const int fit = a.CS > 1 ? int8_cluster_capacity(a.CS) * a.CS : sms;
     const int grid = fit > 0 ? fit : sms / a.CS * a.CS;
     switch (MT) {
-        case 1: return launch_in<1>(a, map, grid, smem, s);
-        case 2: return launch_in<2>(a, map, grid, smem, s);
-        case 3: return launch_in<3>(a, map, grid, smem, s);
-        default: return launch_in<4>(a, map, grid, smem, s);
+        case 1: return launch_in<1>(a, maps, grid, smem, s);
+        case 2: return launch_in<2>(a, maps, grid, smem, s);
+        case 3: return launch_in<3>(a, maps, grid, smem, s);
+        default: return launch_in<4>(a, maps, grid, smem, s);
     }
 }
 
 cudaError_t launch_int8_experts_out(X8Out a, const CUtensorMap* maps, cudaStream_t s) {
-    const int stage = kXTile + (a.NB <= 16 ? 16 : a.NB <= 32 ? 32 : 64) * 128;
+    const int stage = kXTile + (128 << a.lgNB);
     const int room = (kMaxSmem - 1024 - (int)sizeof(XoShared) - (a.TT + 1) * 512) / stage;
     a.stages = room < kXoMaxStages ? room : kXoMaxStages;
     const size_t smem = 1024 + (size_t)a.stages * stage + (size_t)(a.TT + 1) * 512 + sizeof(XoShared);
@@ -1009,8 +1077,8 @@ cudaError_t launch_int8_experts_out(X8Out a, const CUtensorMap* maps, cudaStream
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute at[2];
-    const int grid = a.slabs * ((a.T + a.TT - 1) / a.TT) * a.S;
-    cudaLaunchConfig_t cfg = x8_config(grid, kXoThreads, smem, s, at, a.S);
+    cudaLaunchConfig_t cfg = x8_config(a.slabs * a.S, kXoThreads, smem, s, at, a.S);
+    cfg.gridDim.y = (unsigned)((a.T + a.TT - 1) / a.TT);
     return cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], maps[3], a);
 }
 

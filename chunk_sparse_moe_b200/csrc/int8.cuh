@@ -201,15 +201,15 @@ __device__ __forceinline__ void quantize_row(const T* __restrict__ v, int K, int
 // is the way through one row); many take fewer threads a row, four chunks each.
 constexpr int kQThreads = 256;
 struct QuantPlan {
-    int W, C;
+    int lgW, C;    // W = 2^lgW
 };
 inline QuantPlan quantize_plan(int rows, int K, int elem_bytes) {
     const int V = 16 / elem_bytes;
-    QuantPlan p{kQThreads, 0};
+    QuantPlan p{8, 0};
     if (K % V != 0 || K / V > 8 * kQThreads) return p;
     p.C = K / V > 4 * kQThreads ? 8 : (rows <= 296 && K / V <= 2 * kQThreads ? 2 : 4);
-    p.W = 32;
-    while (p.W * p.C < K / V) p.W *= 2;
+    p.lgW = 5;
+    while ((p.C << p.lgW) < K / V) ++p.lgW;
     return p;
 }
 

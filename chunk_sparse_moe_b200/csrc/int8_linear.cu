@@ -36,22 +36,22 @@
 namespace bffn {
 
 template <typename T, int C>
-__global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(const T* __restrict__ v, int rows, int K, int W,
+__global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(const T* __restrict__ v, int rows, int K, int lgW,
                                                                   int8_t* __restrict__ q, float* __restrict__ scale) {
     __shared__ uint32_t red[8];
     griddep_wait();
     griddep_launch_dependents();
-    const int g = threadIdx.x / W;   // the block's group of W threads
-    const long long row = (long long)blockIdx.x * (kQThreads / W) + g;
+    const int W = 1 << lgW, g = threadIdx.x >> lgW;   // the block's group of W threads
+    const long long row = ((long long)blockIdx.x << (8 - lgW)) + g;
     if (row >= rows) return;
-    quantize_row<T, C>(v + row * K, K, q + row * K, scale + row, W, threadIdx.x - g * W, 1 + g, red + g * (W / 32));
+    quantize_row<T, C>(v + row * K, K, q + row * K, scale + row, W, threadIdx.x & (W - 1), 1 + g, red + (g << lgW >> 5));
 }
 
 namespace {
 template <typename T>
 cudaError_t launch_quantize_t(const T* v, int rows, int K, int8_t* q, float* scale, cudaStream_t s) {
     const QuantPlan p = quantize_plan(rows, K, (int)sizeof(T));
-    const int per = kQThreads / p.W;
+    const int per = kQThreads >> p.lgW;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((rows + (long long)per - 1) / per));
     cfg.blockDim = dim3(kQThreads);
@@ -61,10 +61,10 @@ cudaError_t launch_quantize_t(const T* v, int rows, int K, int8_t* q, float* sca
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (p.C == 0) return cudaLaunchKernelEx(&cfg, quantize_rows_kernel<T, 0>, v, rows, K, p.W, q, scale);
-    if (p.C == 2) return cudaLaunchKernelEx(&cfg, quantize_rows_kernel<T, 2>, v, rows, K, p.W, q, scale);
-    if (p.C == 4) return cudaLaunchKernelEx(&cfg, quantize_rows_kernel<T, 4>, v, rows, K, p.W, q, scale);
-    return cudaLaunchKernelEx(&cfg, quantize_rows_kernel<T, 8>, v, rows, K, p.W, q, scale);
+    if (p.C == 0) return cudaLaunchKernelEx(&cfg, quantize_rows_kernel<T, 0>, v, rows, K, p.lgW, q, scale);
+    if (p.C == 2) return cudaLaunchKernelEx(&cfg, quantize_rows_kernel<T, 2>, v, rows, K, p.lgW, q, scale);
+    if (p.C == 4) return cudaLaunchKernelEx(&cfg, quantize_rows_kernel<T, 4>, v, rows, K, p.lgW, q, scale);
+    return cudaLaunchKernelEx(&cfg, quantize_rows_kernel<T, 8>, v, rows, K, p.lgW, q, scale);
 }
 }  // namespace
 
@@ -105,9 +105,9 @@ int8_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
     IlShared& sh = *reinterpret_cast<IlShared*>(smem + (size_t)a.stages * stage_bytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = S > 1 ? (int)cluster_ctarank() : 0;
-    const int first = S > 1 ? (int)(blockIdx.x / S) : (int)blockIdx.x;
-    const int step = S > 1 ? (int)(gridDim.x / S) : (int)gridDim.x;
-    const int kb0 = (int)((long long)a.KB * rank / S), kb1 = (int)((long long)a.KB * (rank + 1) / S);
+    const int first = S > 1 ? (int)cluster_id_x() : (int)blockIdx.x;
+    const int step = (int)gridDim.x;   // (S > 1: a cluster has one tile)
+    const int kb0 = a.kb_lo[rank], kb1 = a.kb_lo[rank + 1];
     const int tiles = a.tiles_o * a.tiles_t;
 
     if (threadIdx.x == 0) {
@@ -304,7 +304,7 @@ int8_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
                 if (o < a.O) il_put(y + (size_t)c * a.O, fmaf((float)v * sw, st, b));
             }
         }
-        cluster_barrier_sync();   // no block leaves while its partial sums may be read
+        cluster_barrier_sync_relaxed();   // no block leaves while its partial sums may be read
     }
     tc_fence_before();
     __syncthreads();
@@ -400,6 +400,7 @@ cudaError_t launch_int8_linear(IlArgs a, const CUtensorMap* maps, bool bf16_out,
     const int stage = kIlABytes + a.N * 128;
     a.stages = kIlRing / stage < kIlMaxStages ? kIlRing / stage : kIlMaxStages;
     const int tiles = a.tiles_o * a.tiles_t;
+    for (int r = 0; r <= a.S; ++r) a.kb_lo[r] = (int)((long long)a.KB * r / a.S);
     const int grid = a.S > 1 ? tiles * a.S : (tiles < sms ? tiles : sms);
     return bf16_out ? launch_il<__nv_bfloat16>(a, maps, grid, s) : launch_il<float>(a, maps, grid, s);
 }

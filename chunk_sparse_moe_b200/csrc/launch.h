@@ -144,6 +144,7 @@ struct IlArgs {
     int N, S;                 // tokens per tile, blocks per tile (K split)
     int tiles_o, tiles_t;
     int stages;               // set by the launcher
+    int kb_lo[9];             // first K block of each of the S blocks (set by the launcher)
     unsigned long long wait_ns;
 };
 int int8_cluster_capacity(int S);
@@ -172,15 +173,15 @@ struct X8In {
     const float* s_in;        // [E, d_e]
     const float* b_in;        // [E, d_e] or nullptr
     Ctl* ctl;
-    int E, d_e;
+    int T, E, d_e;
     int KB;                   // d_h / 128
-    int N;                    // tokens per tile
+    int lgN;                  // 2^lgN tokens per tile, at most
     int CS;                   // blocks per cluster
     int stages;               // set by the launcher
     unsigned long long wait_ns;
 };
-// map: W_in [E * d_e, d_h] (box {128, 128})
-cudaError_t launch_int8_experts_in(X8In a, const CUtensorMap& map, int sms, cudaStream_t s);
+// maps: W_in [E * d_e, d_h] (box {128, 128}) and xq [T, d_h] (box {128, 2^lgN}, used when T <= 2^lgN)
+cudaError_t launch_int8_experts_in(X8In a, const CUtensorMap* maps, int sms, cudaStream_t s);
 
 struct X8Out {
     X8Bufs w;
@@ -192,7 +193,7 @@ struct X8Out {
     int KBe;                  // d_e / 128
     int slabs;                // d_h / 128
     int TT;                   // tokens per tile (a multiple of 32)
-    int NB;                   // pairs multiplied at a time (16, 32 or 64)
+    int lgNB;                 // 2^lgNB pairs multiplied at a time, at most (16, 32 or 64)
     int S;                    // blocks per cluster
     int stages;               // set by the launcher
     unsigned long long wait_ns;
