@@ -161,6 +161,22 @@ __device__ __forceinline__ XiItem xi_item(const XiShared& sh, int E, int i) {
     return it;
 }
 
+// The same for the tile behind i0's (whose expert is known), by one thread: the next tiles
+// of a block are a grid apart.
+__device__ __forceinline__ XiItem xi_item_from(const XiShared& sh, int E, int i, int e0) {
+    int lo = e0, hi = E;
+    while (hi - lo > 1) {
+        const int m = (lo + hi) >> 1;
+        if (sh.first[m] <= i) lo = m;
+        else hi = m;
+    }
+    XiItem it;
+    it.e = lo;
+    it.base = (i - sh.first[lo]) * sh.per[lo];
+    it.rows = min(sh.per[lo], sh.cnt[lo] - it.base);
+    return it;
+}
+
 // all threads of the named barrier agree: true when every one's v is
 __device__ __forceinline__ bool bar_all(int id, bool v) {
     uint32_t r;
@@ -315,31 +331,31 @@ int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_co
     const int kb0 = a.KB * sub >> lgS, kb1 = a.KB * (sub + 1) >> lgS;
 
     if (warp == 0) {
-        const uint64_t pol = policy_evict_normal();
-        int st = 0, issued = 0;
-        uint32_t ph = 0;
-        bool ok = true;
-        for (int i = first; i < tiles && ok; i += step) {
-            const XiItem it = xi_item(sh, a.E, i);
-            for (int kb = kb0; kb < kb1; ++kb) {
-                ok = wait_bar_warp(&sh.empty[st], ph ^ 1u, limit, &sh.abort, a.ctl, kWaitEmpty);
-                if (!ok) break;
-                if (lane == 0) {
+        XiItem it = {0, 0, 0};
+        if (first < tiles) it = xi_item(sh, a.E, first);
+        // (elect.sync, not lane 0: what one elected lane runs is issued at twice the rate)
+        if (elect_one()) {
+            const uint64_t pol = policy_evict_normal();
+            int st = 0, issued = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int i = first; i < tiles && ok; i += step) {
+                if (i != first) it = xi_item_from(sh, a.E, i, it.e);
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    ok = wait_bar(&sh.empty[st], ph ^ 1u, limit, &sh.abort, a.ctl, kWaitEmpty);
+                    if (!ok) break;
                     mbar_arrive_expect_tx(&sh.full[st], (uint32_t)a_bytes);
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt)
                         tma_load_2d(smem + (size_t)st * stage_bytes + mt * kXTile, &tm_w, &sh.full[st], kb * 128,
                                     it.e * a.d_e + mt * 128, pol);
-                }
-                __syncwarp();
-                ++issued;
-                if (++st == a.stages) {
-                    st = 0;
-                    ph ^= 1u;
+                    ++issued;
+                    if (++st == a.stages) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
                 }
             }
-        }
-        if (lane == 0) {
             // every load issued has landed before the block may end
             const int in_ring = min(issued, a.stages);
             for (int i = 0; i < in_ring; ++i) {
@@ -350,7 +366,7 @@ int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_co
         __syncwarp();
     } else if (warp == 2 || warp == 3 || warp >= 12) {
         if (dense) {
-            if (warp == 2 && lane == 0) {
+            if (warp == 2 && elect_one()) {
                 const uint64_t pol = policy_evict_normal();
                 int st = 0, issued = 0;
                 uint32_t ph = 0;
@@ -435,25 +451,23 @@ int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_co
         __syncwarp();
     } else if (warp == 1) {
         const uint64_t desc0 = sw128_kmajor_desc(smem_u32(smem));
-        int st = 0, buf = 0;
-        uint32_t ph = 0, bph = 0, got_w = 0, got_x = 0;   // (got: the next stage's barriers, tested ahead)
-        bool ok = true;
-        for (int i = first; i < tiles && ok; i += step) {
-            const XiItem it = xi_item(sh, a.E, i);
-            const uint32_t idesc = idesc_i8_s32(128, ((dense ? a.T : it.rows) + 15) & ~15);
-            ok = wait_bar_warp(&sh.acc_empty[buf], bph ^ 1u, limit, &sh.abort, a.ctl, kWaitAccEmpty);
-            if (!ok) break;
-            tc_fence_after();
-            for (int kb = kb0; kb < kb1; ++kb) {
-                ok = wait_tested(got_w, &sh.full[st], ph, limit, &sh.abort, a.ctl, kWaitFullW) &&
-                     wait_tested(got_x, &sh.gathered[st], ph, limit, &sh.abort, a.ctl, kWaitFullW);
+        XiItem it = {0, 0, 0};
+        if (first < tiles) it = xi_item(sh, a.E, first);
+        if (elect_one()) {
+            int st = 0, buf = 0;
+            uint32_t ph = 0, bph = 0;
+            bool ok = true;
+            for (int i = first; i < tiles && ok; i += step) {
+                if (i != first) it = xi_item_from(sh, a.E, i, it.e);
+                const uint32_t idesc = idesc_i8_s32(128, ((dense ? a.T : it.rows) + 15) & ~15);
+                ok = wait_bar(&sh.acc_empty[buf], bph ^ 1u, limit, &sh.abort, a.ctl, kWaitAccEmpty);
                 if (!ok) break;
                 tc_fence_after();
-                const int nst = st + 1 == a.stages ? 0 : st + 1;
-                const uint32_t nph = nst == 0 ? ph ^ 1u : ph;
-                got_w = mbar_test_wait(&sh.full[nst], nph);
-                got_x = mbar_test_wait(&sh.gathered[nst], nph);
-                if (elect_one()) {
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    ok = wait_bar(&sh.full[st], ph, limit, &sh.abort, a.ctl, kWaitFullW) &&
+                         wait_bar(&sh.gathered[st], ph, limit, &sh.abort, a.ctl, kWaitFullW);
+                    if (!ok) break;
+                    tc_fence_after();
                     const uint64_t ad = desc0 + (uint64_t)((uint32_t)st * (uint32_t)stage_bytes >> 4);
                     const uint64_t bd = ad + (uint64_t)(a_bytes >> 4);
 #pragma unroll
@@ -464,18 +478,18 @@ int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_co
                                     idesc, kb > kb0 || k > 0);
                     umma_commit(&sh.empty[st]);
                     if (kb == kb1 - 1) umma_commit(&sh.acc_full[buf]);
+                    if (++st == a.stages) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
                 }
-                __syncwarp();
-                st = nst;
-                ph = nph;
+                buf ^= 1;
+                if (buf == 0) bph ^= 1u;
             }
-            buf ^= 1;
-            if (buf == 0) bph ^= 1u;
+            // no MMA is in flight when the accumulators are given back
+            umma_commit(&sh.mma_done);
+            wait_bar_drain(&sh.mma_done, 0u, limit, a.ctl);
         }
-        // no MMA is in flight when the accumulators are given back
-        if (elect_one()) umma_commit(&sh.mma_done);
-        __syncwarp();
-        if (lane == 0) wait_bar_drain(&sh.mma_done, 0u, limit, a.ctl);
         __syncwarp();
     } else {   // warps 4 .. 11
         const int q = warp & 3, group = (warp - 4) >> 2, ch = q * 32 + lane;
@@ -783,7 +797,7 @@ int8_experts_out_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_c
     if (warp == 0 || warp == 2) {
         // Warp 0 loads weight tiles, warp 2 the pairs' rows of h: one thread issues a TMA
         // copy every few hundred cycles, so the two operands have an issuer each.
-        if (lane == 0) {
+        if (elect_one()) {
             uint64_t* const full = sh.full[warp >> 1];
             const uint64_t pol = policy_evict_normal();
             int st = 0, issued = 0;
@@ -826,31 +840,20 @@ int8_experts_out_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_c
         }
         __syncwarp();
     } else if (warp == 1) {
-        // One entry after another; the barriers of the next stage and accumulator are tested
-        // before the present one's MMAs are issued, so that in the steady state nothing
-        // is waited for (waiting in turn for each made 600 cycles an entry).
         const uint64_t desc0 = sw128_kmajor_desc(smem_u32(smem));
-        int st = 0, buf = 0;
-        uint32_t ph = 0, bph = 0;
-        bool ok = true;
-        uint32_t got_w = 0, got_h = 0, got_a = 0;
-        for (int m = m0; m < m1 && ok; ++m) {
-            const uint32_t idesc = idesc_i8_s32(128, (int)((sh.ent[m] >> 16 & 255u) + 16) & ~15);
-            ok = wait_tested(got_a, &sh.acc_empty[buf], bph ^ 1u, limit, &sh.abort, a.ctl, kWaitAccEmpty);
-            if (!ok) break;
-            const int nbuf = buf + 1 == kXoAcc ? 0 : buf + 1;
-            const uint32_t nbph = nbuf == 0 ? bph ^ 1u : bph;
-            for (int kb = 0; kb < a.KBe; ++kb) {
-                ok = wait_tested(got_w, &sh.full[0][st], ph, limit, &sh.abort, a.ctl, kWaitFullW) &&
-                     wait_tested(got_h, &sh.full[1][st], ph, limit, &sh.abort, a.ctl, kWaitFullH);
+        if (elect_one()) {
+            int st = 0, buf = 0;
+            uint32_t ph = 0, bph = 0;
+            bool ok = true;
+            for (int m = m0; m < m1 && ok; ++m) {
+                const uint32_t idesc = idesc_i8_s32(128, (int)((sh.ent[m] >> 16 & 255u) + 16) & ~15);
+                ok = wait_bar(&sh.acc_empty[buf], bph ^ 1u, limit, &sh.abort, a.ctl, kWaitAccEmpty);
                 if (!ok) break;
-                tc_fence_after();
-                const int nst = st + 1 == a.stages ? 0 : st + 1;
-                const uint32_t nph = nst == 0 ? ph ^ 1u : ph;
-                got_w = mbar_test_wait(&sh.full[0][nst], nph);
-                got_h = mbar_test_wait(&sh.full[1][nst], nph);
-                if (kb == a.KBe - 1) got_a = mbar_test_wait(&sh.acc_empty[nbuf], nbph ^ 1u);
-                if (elect_one()) {
+                for (int kb = 0; kb < a.KBe; ++kb) {
+                    ok = wait_bar(&sh.full[0][st], ph, limit, &sh.abort, a.ctl, kWaitFullW) &&
+                         wait_bar(&sh.full[1][st], ph, limit, &sh.abort, a.ctl, kWaitFullH);
+                    if (!ok) break;
+                    tc_fence_after();
                     const uint64_t ad = desc0 + (uint64_t)((uint32_t)st * (uint32_t)stage_bytes >> 4);
                     const uint64_t bd = ad + (kXTile >> 4);
 #pragma unroll
@@ -858,17 +861,19 @@ int8_experts_out_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_c
                         umma_i8(tmem + (uint32_t)(buf * kXoNB), ad + 2 * k, bd + 2 * k, idesc, kb > 0 || k > 0);
                     umma_commit(&sh.empty[st]);
                     if (kb == a.KBe - 1) umma_commit(&sh.acc_full[buf]);
+                    if (++st == a.stages) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
                 }
-                __syncwarp();
-                st = nst;
-                ph = nph;
+                if (++buf == kXoAcc) {
+                    buf = 0;
+                    bph ^= 1u;
+                }
             }
-            buf = nbuf;
-            bph = nbph;
+            umma_commit(&sh.mma_done);
+            wait_bar_drain(&sh.mma_done, 0u, limit, a.ctl);
         }
-        if (elect_one()) umma_commit(&sh.mma_done);
-        __syncwarp();
-        if (lane == 0) wait_bar_drain(&sh.mma_done, 0u, limit, a.ctl);
         __syncwarp();
     } else if (warp >= 4 && warp < 8) {
         // What the epilogue needs of each entry (the four warps in turn, reading kAhead of their

@@ -97,7 +97,8 @@ __device__ __forceinline__ void il_put(__nv_bfloat16* y, float v) { *y = __float
 
 template <typename OutT>
 __global__ void __launch_bounds__(kIlThreads, 1)
-int8_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, const IlArgs a) {
+int8_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                   const __grid_constant__ IlArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int N = a.N, S = a.S;
@@ -137,7 +138,8 @@ int8_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
     const uint64_t limit = a.wait_ns;
 
     if (warp == 0) {
-        if (lane == 0) {
+        // (elect.sync, not lane 0: what one elected lane runs is issued at twice the rate)
+        if (elect_one()) {
             const uint64_t pol = policy_evict_normal();
             int st = 0;
             uint32_t ph = 0;
@@ -183,24 +185,22 @@ int8_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
                 wait_bar_drain(&sh.full[st], (uint32_t)(nth & 1), limit, a.ctl);
             }
         }
+        __syncwarp();
     } else if (warp == 1) {
         const uint32_t idesc = idesc_i8_s32(128, N);
         const uint64_t desc0 = sw128_kmajor_desc(smem_u32(smem));
-        int st = 0, buf = 0;
-        uint32_t ph = 0, bph = 0, got = 0;
-        bool ok = true;
-        for (int tile = first; tile < tiles && ok; tile += step) {
-            ok = wait_bar_warp(&sh.acc_empty[buf], bph ^ 1u, limit, &sh.abort, a.ctl, kWaitAccEmpty);
-            if (!ok) break;
-            tc_fence_after();
-            for (int kb = kb0; kb < kb1; ++kb) {
-                ok = wait_tested(got, &sh.full[st], ph, limit, &sh.abort, a.ctl, kWaitFullW);
+        if (elect_one()) {
+            int st = 0, buf = 0;
+            uint32_t ph = 0, bph = 0;
+            bool ok = true;
+            for (int tile = first; tile < tiles && ok; tile += step) {
+                ok = wait_bar(&sh.acc_empty[buf], bph ^ 1u, limit, &sh.abort, a.ctl, kWaitAccEmpty);
                 if (!ok) break;
                 tc_fence_after();
-                const int nst = st + 1 == a.stages ? 0 : st + 1;
-                const uint32_t nph = nst == 0 ? ph ^ 1u : ph;
-                got = mbar_test_wait(&sh.full[nst], nph);   // the next stage's, tested ahead
-                if (elect_one()) {
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    ok = wait_bar(&sh.full[st], ph, limit, &sh.abort, a.ctl, kWaitFullW);
+                    if (!ok) break;
+                    tc_fence_after();
                     const uint64_t ad = desc0 + (uint64_t)((uint32_t)st * (uint32_t)stage_bytes >> 4);
                     const uint64_t bd = ad + (kIlABytes >> 4);
 #pragma unroll
@@ -208,18 +208,18 @@ int8_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
                         umma_i8(tmem + (uint32_t)(buf * N), ad + 2 * k, bd + 2 * k, idesc, kb > kb0 || k > 0);
                     umma_commit(&sh.empty[st]);
                     if (kb == kb1 - 1) umma_commit(&sh.acc_full[buf]);
+                    if (++st == a.stages) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
                 }
-                __syncwarp();
-                st = nst;
-                ph = nph;
+                buf ^= 1;
+                if (buf == 0) bph ^= 1u;
             }
-            buf ^= 1;
-            if (buf == 0) bph ^= 1u;
+            // no MMA is in flight when the accumulators are given back
+            umma_commit(&sh.mma_done);
+            wait_bar_drain(&sh.mma_done, 0u, limit, a.ctl);
         }
-        // no MMA is in flight when the accumulators are given back
-        if (elect_one()) umma_commit(&sh.mma_done);
-        __syncwarp();
-        if (lane == 0) wait_bar_drain(&sh.mma_done, 0u, limit, a.ctl);
         __syncwarp();
     } else if (warp >= 4) {
         griddep_wait();   // the token scales
