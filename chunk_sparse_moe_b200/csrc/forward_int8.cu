@@ -192,10 +192,8 @@ __device__ __forceinline__ bool bar_all(int id, bool v) {
 }
 
 __device__ __forceinline__ void tmem_ld_piece(uint32_t taddr, int (&v)[8]) {
-    uint32_t u[8];
-    tmem_ld_32x32b_x8(taddr, u);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = (int)u[j];
+    // (no copy: the registers hold their values only after tmem_ld_wait)
+    tmem_ld_32x32b_x8(taddr, reinterpret_cast<uint32_t (&)[8]>(v));
 }
 
 // What the epilogue does with PW columns (tokens) of int32 sums: h, its scale over all of
