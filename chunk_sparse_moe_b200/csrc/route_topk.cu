@@ -185,11 +185,16 @@ __device__ __forceinline__ void tk_choice_keys(const TkArgs& a, const float (&z)
 #pragma unroll
         for (int j = 0; j < NJ; ++j) s[j] *= inv;
     }
+    float b[NJ];
+    if (brow != nullptr) {
+        tk_load<NJ>(brow, a.E, lane, 0.f, b);
+    } else {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) b[j] = 0.f;
+    }
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-        const int e = lane * NJ + j;
-        const float b = (brow != nullptr && e < a.E) ? __ldg(brow + e) : 0.f;
-        const R c = s[j] + (R)b;
+        const R c = s[j] + (R)b[j];
         key[j] = (z[j] > -INFINITY && c > -INFINITY) ? K::of(c) : typename K::Bits(0);
     }
 }
@@ -363,6 +368,36 @@ __device__ __forceinline__ bool tk_pick(const TkArgs& a, const float (&z)[NJ], i
     return close;
 }
 
+// tk_pick for scored keys, quicker: the three lowest bits of a key give way to the place of
+// the expert in its lane, so that the warp's maximum names it.  That moves a value by less
+// than 2^-20 of itself, which the doubtful gap covers; a tie orders by that place first, so
+// every gap that small is doubtful here and the row is picked again by tk_pick.
+template <int NJ>
+__device__ __forceinline__ bool tk_pick_quick(const TkArgs& a, int lane, const uint32_t (&key)[NJ], int& my_id) {
+    uint32_t k3[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) k3[j] = key[j] != 0 ? (key[j] & ~7u) | (uint32_t)(7 - j) : 0u;
+    my_id = -1;
+    float last = INFINITY;
+    for (int n = 0; n <= a.k; ++n) {
+        uint32_t best = k3[0];
+#pragma unroll
+        for (int j = 1; j < NJ; ++j) best = max(best, k3[j]);
+        const uint32_t m = Key32::warp_max(best);
+        if (m == 0) break;
+        const float v = Key32::value(m);
+        if (!(last - v > 6e-6f * (1.f + fabsf(v)))) return true;
+        if (n == a.k) break;
+        last = v;
+        const int src = __ffs(__ballot_sync(0xffffffffu, best == m)) - 1;
+        if (lane == n) my_id = src * NJ + 7 - (int)(m & 7u);
+        const uint32_t mine = lane == src ? m : 0xffffffffu;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) k3[j] = k3[j] == mine ? 0u : k3[j];
+    }
+    return false;
+}
+
 template <int NJ, class K>
 __device__ __forceinline__ bool tk_choose(const TkArgs& a, const float (&z)[NJ], int lane, void* srow, bool scored,
                                           int& my_id, float& m, float& sum) {
@@ -381,6 +416,9 @@ __device__ __forceinline__ bool tk_choose(const TkArgs& a, const float (&z)[NJ],
     } else {
 #pragma unroll
         for (int j = 0; j < NJ; ++j) key[j] = z[j] > -INFINITY ? K::of(z[j]) : typename K::Bits(0);
+    }
+    if constexpr (sizeof(typename K::Bits) == 4) {
+        if (scored && !close && !tk_pick_quick<NJ>(a, lane, key, my_id)) return false;
     }
     const bool c2 = tk_pick<NJ, K>(a, z, lane, key, scored, my_id);
     return close || c2;
@@ -447,17 +485,23 @@ __global__ void __launch_bounds__(kTkWarps * 32) route_topk_kernel(const T* __re
         a.weights[(size_t)t * a.k + lane] = w;
     }
     if (a.gates == nullptr) return;
-    // the dense row: zeros and the chosen weights meet in shared memory
+    // the dense row: zeros and the chosen weights meet in shared memory (rows of float4)
     float* srow = reinterpret_cast<float*>(stage[warp]);
-    float g[NJ];
+    constexpr int kQuads = (NJ * 32 + 127) / 128;
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) srow[lane * NJ + j] = 0.f;
+    for (int i = 0; i < kQuads; ++i) reinterpret_cast<float4*>(srow)[i * 32 + lane] = make_float4(0.f, 0.f, 0.f, 0.f);
     __syncwarp();
     if (have) srow[id] = w;
     __syncwarp();
+    float* grow = a.gates + (size_t)t * a.E;
+    if ((a.E & 3) == 0) {   // (every row is then 16-byte aligned)
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) g[j] = srow[lane * NJ + j];
-    tk_store<NJ>(a.gates + (size_t)t * a.E, a.E, lane, g);
+        for (int i = 0; i < kQuads; ++i)
+            if ((i * 32 + lane) * 4 < a.E)
+                reinterpret_cast<float4*>(grow)[i * 32 + lane] = reinterpret_cast<const float4*>(srow)[i * 32 + lane];
+    } else {
+        for (int e = lane; e < a.E; e += 32) grow[e] = srow[e];
+    }
 }
 
 // The gradient of the weights with respect to the logits, the choice held fixed.
