@@ -18,6 +18,12 @@ language-model head: how many tokens a step accepts is a synthetic input (see
 ``workloads.accept_lengths``), so the driver measures the verifier's cost per
 drafted and per accepted token.  Only orchestration lives here; every step of
 the arithmetic runs in the library's kernels.
+
+A layer may also route by top-k (``TopK``: its logits are an 8-bit product with
+``W_r``) and hold its experts in 8 bits (int8 ``W_in`` and ``W_out`` with their channel
+scales, as ``quantize_int8`` lays them out): then its step is ``int8_linear``,
+``route_topk`` and ``forward_int8``.  Either can go with the other form of its
+counterpart.
 """
 from __future__ import annotations
 
@@ -26,7 +32,19 @@ from typing import List, Optional, Sequence
 
 import torch
 
-from .api import Workspace, forward
+from .api import Workspace, forward, forward_int8, int8_linear, route, route_topk
+
+
+@dataclass
+class TopK:
+    """How a layer chooses its experts (see ``route_topk``)."""
+    k: int
+    scores: str = "softmax"
+    bias: Optional[torch.Tensor] = None      # [E] fp32, added to the scores for the choice only
+    n_group: int = 1
+    topk_group: Optional[int] = None
+    renormalize: bool = True
+    scale: float = 1.0
 
 
 @dataclass
@@ -43,6 +61,16 @@ class Layer:
     ln_eps: float = 1e-5                     # LayerNorm epsilon
     b_in: Optional[torch.Tensor] = None      # [E, d_e] fp32 expert fc1 biases
     b_out: Optional[torch.Tensor] = None     # [E, d_h] fp32 expert fc2 biases
+    # 8-bit experts: W_in and W_out are int8, these are their channel scales
+    s_in: Optional[torch.Tensor] = None      # [E, d_e] fp32
+    s_out: Optional[torch.Tensor] = None     # [E, d_h] fp32
+    # top-k routing: W_r [E, d_h] is int8 with the channel scales s_r, b_r its bias
+    topk: Optional[TopK] = None
+    s_r: Optional[torch.Tensor] = None       # [E] fp32
+
+    @property
+    def int8(self) -> bool:
+        return self.W_in.dtype == torch.int8
 
 
 class Verifier:
@@ -59,10 +87,42 @@ class Verifier:
         E, d_e, d_h = self.layers[0].W_in.shape
         self.d_h = d_h
         device = device or self.layers[0].W_in.device
-        self.ws = [Workspace.for_shapes(n, L.W_in.shape[2], L.W_in.shape[0], L.W_in.shape[1], n, dtype,
-                                        L.gates is None, device, with_bias=L.b_out is not None)
-                   for L in self.layers]
+        for L in self.layers:
+            if L.int8 and (L.s_in is None or L.s_out is None):
+                raise ValueError("8-bit experts need their scales s_in and s_out")
+            if L.topk is not None and (L.gates is not None or L.W_r is None or L.s_r is None):
+                raise ValueError("a top-k layer needs an int8 W_r with its scales s_r, and no gates")
+        self.ws = [self._workspace(L, dtype, device) for L in self.layers]
+        # what a layer's routing writes on the way, where ``forward`` does not route itself
+        self.routing = [self._routing_buffers(L, device) for L in self.layers]
         self.h = [torch.empty((n, d_h), dtype=dtype, device=device) for _ in range(2)]
+
+    def _workspace(self, L: Layer, dtype: torch.dtype, device) -> Workspace:
+        E, d_e, d_h = L.W_in.shape
+        if L.int8:
+            return Workspace.for_forward_int8(self.n, d_h, E, d_e, device)
+        return Workspace.for_shapes(self.n, d_h, E, d_e, self.n, dtype, L.gates is None and L.topk is None, device,
+                                    with_bias=L.b_out is not None)
+
+    def _routing_buffers(self, L: Layer, device):
+        E, f32 = L.W_in.shape[0], torch.float32
+        buf = lambda cols, dtype: torch.empty((self.n, cols), dtype=dtype, device=device)  # noqa: E731
+        if L.topk is not None:   # the product's scratch, logits, gates, ids, weights
+            return (Workspace.for_int8_linear(self.n, L.W_r.shape[1], E, device), buf(E, f32), buf(E, f32),
+                    buf(L.topk.k, torch.int32), buf(L.topk.k, f32))
+        return buf(E, f32) if L.int8 and L.gates is None else None
+
+    def _gates(self, i: int, L: Layer, h: torch.Tensor) -> Optional[torch.Tensor]:
+        """The layer's gates, or None where ``forward`` runs the layer's router itself."""
+        if L.topk is not None:
+            ws, logits, *out = self.routing[i]
+            int8_linear(h, L.W_r, L.s_r, bias=L.b_r, y=logits, workspace=ws)
+            c = L.topk
+            return route_topk(logits, c.k, scores=c.scores, bias=c.bias, n_group=c.n_group, topk_group=c.topk_group,
+                              renormalize=c.renormalize, scale=c.scale, out=out)[0]
+        if L.gates is None and L.int8:
+            return route(h, L.W_r, L.gamma, L.eps, b_r=L.b_r, out=self.routing[i])
+        return L.gates
 
     def step(self, x: torch.Tensor) -> torch.Tensor:
         """Hidden states [n, d_h] of the chunk after every layer (a buffer of the
@@ -72,8 +132,11 @@ class Verifier:
             # the layer's output goes to the buffer its input is not in
             kw = dict(y=self.h[i % 2], workspace=self.ws[i], b_in=L.b_in, b_out=L.b_out,
                       ln_weight=L.ln_gamma, ln_bias=L.ln_beta, ln_eps=L.ln_eps)
-            if L.gates is not None:
-                h = forward(h, L.W_in, L.W_out, self.n, gates=L.gates, **kw)
+            gates = self._gates(i, L, h)
+            if L.int8:
+                h = forward_int8(h, gates, L.W_in, L.s_in, L.W_out, L.s_out, **kw)
+            elif gates is not None:
+                h = forward(h, L.W_in, L.W_out, self.n, gates=gates, **kw)
             else:
                 h = forward(h, L.W_in, L.W_out, self.n, W_r=L.W_r, b_r=L.b_r, gamma=L.gamma, eps=L.eps, **kw)
         return h

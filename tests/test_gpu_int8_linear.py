@@ -174,6 +174,28 @@ def test_linear_graph_and_stream():
     assert bffn.device_status(ws) == (0, 0)
 
 
+@pytest.mark.parametrize("T", [1, 64, 600])
+def test_linear_reads_what_the_kernel_before_it_wrote(T):
+    """Weights, scales and tokens written by the kernels right before the call (it loads its first weight
+    tiles early)."""
+    bffn = require_cuda()
+    K, O = 2048, 1024
+    rng = np.random.default_rng(8)
+    sets = [(torch.from_numpy(rng.integers(-127, 128, (O, K)).astype(np.int8)).cuda(), torch.rand(O).cuda(),
+             values((T, K), torch.bfloat16, i).cuda()) for i in range(3)]
+    want = [bffn.int8_linear(x, W, s) for W, s, x in sets]
+    W, s, x = (torch.empty_like(t) for t in sets[0])
+    ws = bffn.Workspace.for_int8_linear(T, K, O)
+    got = []
+    torch.cuda.synchronize()
+    for turn in range(30):
+        for dst, src in zip((x, s, W), (sets[turn % 3][2], sets[turn % 3][1], sets[turn % 3][0])):
+            dst.copy_(src)
+        got.append(bffn.int8_linear(x, W, s, workspace=ws))
+    for turn in range(30):
+        assert torch.equal(got[turn], want[turn % 3])
+
+
 def test_linear_empty_and_refusals():
     bffn = require_cuda()
     W = torch.zeros(8, 64, dtype=torch.int8, device="cuda")
