@@ -456,14 +456,14 @@ blockffn_status blockffn_int8_linear(const void* x, blockffn_dtype dt, const int
     a.T = T;
     a.O = O;
     a.KB = (K + 127) / 128;
-    int8_linear_plan(T, K, O, G, &a.N, &a.S);
-    a.tiles_o = (O + 127) / 128;
+    int8_linear_plan(T, K, O, G, &a.N, &a.S, &a.pair);
+    a.tiles_o = a.pair ? (O + 255) / 256 : (O + 127) / 128;
     a.tiles_t = (T + a.N - 1) / a.N;
     a.stages = 0;
     a.wait_ns = g_wait_ns.load();
     CUtensorMap maps[2];
     if (!make_map_u8(&maps[0], W, (uint64_t)K, (uint64_t)O, 128) ||
-        !make_map_u8(&maps[1], q, (uint64_t)K, (uint64_t)T, (uint32_t)a.N))
+        !make_map_u8(&maps[1], q, (uint64_t)K, (uint64_t)T, a.pair ? 128u : (uint32_t)a.N))
         return fail(BLOCKFFN_ERR_CUDA, "cuTensorMapEncodeTiled failed");
     cudaError_t e = launch_quantize_rows(x, dt == BLOCKFFN_BF16, T, K, q, sx, s);
     if (e != cudaSuccess) return cuda_fail(e, "quantize launch");

@@ -311,6 +311,194 @@ int8_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
     if (warp == 2) tmem_dealloc(tmem, 2 * N);
 }
 
+// Many tiles: a pair of blocks shares a tile of 256 channels x 256 tokens (cta_group::2).  Each
+// block brings its 128 rows of W and half of the token rows, 32 KB a stage for the MMA work
+// that takes a single block 48 KB, and has its 128 channels of all 256 tokens in its own
+// TMEM.  L2's delivery is what bounds the single-block form (about 55 bytes a cycle and SM).
+// The pair's first block issues the MMAs; the loads of both blocks are counted on its
+// barriers, and finished MMAs are reported to both.
+namespace {
+
+constexpr int kIpStages = 6;
+constexpr int kIpStage = 2 * kIlABytes;   // 128 rows of W, 128 token rows
+
+struct IpShared {
+    uint64_t full[kIpStages];             // first block: both blocks' loads of the stage (bytes)
+    uint64_t empty[kIpStages];
+    uint64_t acc_full[2];
+    uint64_t acc_empty[2];                // first block: both blocks' epilogue warps
+    uint64_t mma_done;
+    uint32_t tmem_base;
+    volatile int abort;
+};
+
+}  // namespace
+
+template <typename OutT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kIlThreads, 1)
+int8_linear_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                        const __grid_constant__ IlArgs a) {
+    constexpr int N = 256;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    IpShared& sh = *reinterpret_cast<IpShared*>(smem + kIpStages * kIpStage);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_ctarank();
+    const int first = (int)cluster_id_x(), step = (int)gridDim.x >> 1;
+    const int tiles = a.tiles_o * a.tiles_t;   // of 256 channels, 256 tokens
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kIpStages; ++i) {
+            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.acc_full[i], 1);
+            mbar_init(&sh.acc_empty[i], 16);
+        }
+        mbar_init(&sh.mma_done, 1);
+        fence_mbar_init();
+        sh.abort = 0;
+        prefetch_tmap(&tm_w);
+        prefetch_tmap(&tm_x);
+    }
+    if (warp == 2) tmem_alloc_pair(&sh.tmem_base, 2 * N);
+    tc_fence_before();
+    cluster_barrier_sync();   // barriers of both blocks are set up
+    tc_fence_after();
+    griddep_launch_dependents();
+    const uint32_t tmem = sh.tmem_base;
+    const uint64_t limit = a.wait_ns;
+
+    if (warp == 0) {
+        if (elect_one()) {
+            const uint64_t pol = policy_evict_normal();
+            int st = 0, issued = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            griddep_wait();
+            if (__ldcg(&a.ctl->status) != 0) {
+                sh.abort = 1;
+                ok = false;
+            }
+            const uint32_t full0 = mapa_shared(smem_u32(&sh.full[0]), 0u);   // the first block's
+            for (int tile = first; tile < tiles && ok; tile += step) {
+                const int o = (tile % a.tiles_o * 2 + rank) * 128, t = tile / a.tiles_o * N + rank * 128;
+                for (int kb = 0; kb < a.KB; ++kb) {
+                    ok = wait_bar(&sh.empty[st], ph ^ 1u, limit, &sh.abort, a.ctl, kWaitEmpty);
+                    if (!ok) break;
+                    uint8_t* sp = smem + st * kIpStage;
+                    const uint32_t bar = full0 + 8u * (uint32_t)st;
+                    // (the second block's bytes may be counted before they are expected: the phase
+                    // ends with the arrival that expects them)
+                    if (rank == 0) mbar_arrive_expect_tx(&sh.full[st], 2 * kIpStage);
+                    tma_load_2d_pair(sp, &tm_w, bar, kb * 128, o, pol);
+                    tma_load_2d_pair(sp + kIlABytes, &tm_x, bar, kb * 128, t, pol);
+                    ++issued;
+                    if (++st == kIpStages) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            // every load issued has landed before the pair may end: the first block waits for
+            // both (the second is held by the closing cluster barrier)
+            const int in_ring = rank == 0 ? min(issued, kIpStages) : 0;
+            for (int i = 0; i < in_ring; ++i) {
+                st = st == 0 ? kIpStages - 1 : st - 1;
+                wait_bar_drain(&sh.full[st], (uint32_t)(((issued - 1 - i) / kIpStages) & 1), limit, a.ctl);
+            }
+            // after a timeout the blocks may have stopped at different stages, and loads of the
+            // second one that the first does not expect cannot be waited for: give them time
+            if (sh.abort) {
+                const uint64_t t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1 && rank == 0) {
+        const uint32_t idesc = idesc_i8_s32(256, N);
+        const uint64_t desc0 = sw128_kmajor_desc(smem_u32(smem));
+        if (elect_one()) {
+            int st = 0, buf = 0;
+            uint32_t ph = 0, bph = 0;
+            bool ok = true;
+            for (int tile = first; tile < tiles && ok; tile += step) {
+                ok = wait_bar_cluster(&sh.acc_empty[buf], bph ^ 1u, limit, &sh.abort, a.ctl, kWaitAccEmpty);
+                if (!ok) break;
+                for (int kb = 0; kb < a.KB; ++kb) {
+                    ok = wait_bar(&sh.full[st], ph, limit, &sh.abort, a.ctl, kWaitFullW);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t ad = desc0 + (uint64_t)((uint32_t)(st * kIpStage) >> 4);
+                    const uint64_t bd = ad + (kIlABytes >> 4);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_i8_pair(tmem + (uint32_t)(buf * N), ad + 2 * k, bd + 2 * k, idesc, kb > 0 || k > 0);
+                    umma_commit_pair(&sh.empty[st]);
+                    if (kb == a.KB - 1) umma_commit_pair(&sh.acc_full[buf]);
+                    if (++st == kIpStages) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
+                }
+                buf ^= 1;
+                if (buf == 0) bph ^= 1u;
+            }
+            // no MMA is in flight when the accumulators are given back
+            umma_commit_pair(&sh.mma_done);
+            wait_bar_drain(&sh.mma_done, 0u, limit, a.ctl);
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        griddep_wait();   // the token scales
+        const int q = warp & 3, half = (warp - 4) >> 2, ch = q * 32 + lane;
+        const uint32_t freed = mapa_shared(smem_u32(&sh.acc_empty[0]), 0u);   // (and the next 8 bytes)
+        int buf = 0;
+        uint32_t bph = 0;
+        for (int tile = first; tile < tiles; tile += step) {
+            const int t0 = tile / a.tiles_o * N, o = (tile % a.tiles_o * 2 + rank) * 128 + ch;
+            // lanes 0-15 hold the token scales of a piece's columns
+            auto scales = [&](int c) {
+                const int t = t0 + c + (lane & 15);
+                return c < N && t < a.T ? __ldcg(a.sx + t) : 0.f;
+            };
+            float sx = scales(half * 16);
+            const float sw = o < a.O ? __ldg(a.sw + o) : 0.f;
+            const float b = (a.bias != nullptr && o < a.O) ? __ldg(a.bias + o) : 0.f;
+            if (!wait_bar_warp(&sh.acc_full[buf], bph, limit, &sh.abort, a.ctl, kWaitAccFull)) break;
+            tc_fence_after();
+            const uint32_t tacc = tmem + (uint32_t)(buf * N) + ((uint32_t)(q * 32) << 16);
+            OutT* y = static_cast<OutT*>(a.y) + (size_t)t0 * a.O + o;
+#pragma unroll 1
+            for (int c = half * 16; c < N; c += 32) {
+                uint32_t v[32];
+                tmem_ld_32x32b_x16(tacc + (uint32_t)c, v);
+                const float sx0 = sx;
+                sx = scales(c + 32);
+                tmem_ld_wait();
+                if (c + 32 >= N) {   // the group's last piece: its columns are in registers
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(freed + 8u * (uint32_t)buf);
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float st = __shfl_sync(0xffffffffu, sx0, i);
+                    if (o < a.O && t0 + c + i < a.T)
+                        il_put(y + (size_t)(c + i) * a.O, fmaf((float)(int)v[i] * sw, st, b));
+                }
+            }
+            buf ^= 1;
+            if (buf == 0) bph ^= 1u;
+        }
+    }
+    tc_fence_before();
+    cluster_barrier_sync();   // no block leaves while the pair's MMAs may read it or report to it
+    tc_fence_after();
+    if (warp == 2) tmem_dealloc_pair(tmem, 2 * N);
+}
+
 namespace {
 size_t il_smem(int stages, int N) { return 1024 + (size_t)stages * (kIlABytes + N * 128) + sizeof(IlShared); }
 
@@ -374,7 +562,8 @@ int int8_cluster_capacity(int S) {
 // 128 bytes of K, or the time of its (128 + N) * 128 bytes at about 48 bytes per cycle
 // and SM, and some 1500 cycles of start and epilogue (more where a cluster meets);
 // the pair (N, S) with the smallest time over all waves is taken.
-void int8_linear_plan(int T, int K, int O, int sms, int* N_out, int* S_out) {
+// Pairs of blocks (tiles of 256 x 256) bring 64 KB for what single blocks' 256 x 256 takes 96.
+void int8_linear_plan(int T, int K, int O, int sms, int* N_out, int* S_out, bool* pair_out) {
     const int KB = (K + 127) / 128, tiles_o = (O + 127) / 128;
     double best = 1e30;
     *N_out = 256;
@@ -394,9 +583,46 @@ void int8_linear_plan(int T, int K, int O, int sms, int* N_out, int* S_out) {
             }
         }
     }
+    const int pairs = int8_cluster_capacity(2);
+    *pair_out = false;
+    if (pairs > 0) {
+        const long long tiles = (long long)((O + 255) / 256) * ((T + 255) / 256);
+        const double waves = (double)((tiles + pairs - 1) / pairs);
+        const double cost = waves * (KB * (256.0 * 128.0 / 48.0) + 1024.0) + 2500.0;
+        if (cost < best) {
+            *N_out = 256;
+            *S_out = 1;
+            *pair_out = true;
+        }
+    }
 }
 
+namespace {
+template <typename OutT>
+cudaError_t launch_ip(const IlArgs& a, const CUtensorMap* maps, int grid, cudaStream_t s) {
+    auto kern = int8_linear_pair_kernel<OutT>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kIlThreads);
+    cfg.dynamicSmemBytes = 1024 + (size_t)kIpStages * kIpStage + sizeof(IpShared);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], a);
+}
+}  // namespace
+
 cudaError_t launch_int8_linear(IlArgs a, const CUtensorMap* maps, bool bf16_out, int sms, cudaStream_t s) {
+    if (a.pair) {
+        const int tiles = a.tiles_o * a.tiles_t, fit = int8_cluster_capacity(2);
+        const int grid = 2 * (tiles < fit ? tiles : fit);
+        return bf16_out ? launch_ip<__nv_bfloat16>(a, maps, grid, s) : launch_ip<float>(a, maps, grid, s);
+    }
     const int stage = kIlABytes + a.N * 128;
     a.stages = kIlRing / stage < kIlMaxStages ? kIlRing / stage : kIlMaxStages;
     const int tiles = a.tiles_o * a.tiles_t;

@@ -142,14 +142,15 @@ struct IlArgs {
     int T, O;
     int KB;                   // 128-byte blocks of K
     int N, S;                 // tokens per tile, blocks per tile (K split)
+    bool pair;                // pairs of blocks, tiles of 256 x 256 (cta_group::2)
     int tiles_o, tiles_t;
     int stages;               // set by the launcher
     int kb_lo[9];             // first K block of each of the S blocks (set by the launcher)
     unsigned long long wait_ns;
 };
 int int8_cluster_capacity(int S);
-void int8_linear_plan(int T, int K, int O, int sms, int* N, int* S);
-// maps: W [O, K] (box {128, 128}) and q [T, K] (box {128, N}), bytes, 128-byte swizzle
+void int8_linear_plan(int T, int K, int O, int sms, int* N, int* S, bool* pair);
+// maps: W [O, K] (box {128, 128}) and q [T, K] (box {128, N}; pair: {128, 128}), bytes, 128-byte swizzle
 cudaError_t launch_int8_linear(IlArgs a, const CUtensorMap* maps, bool bf16_out, int sms, cudaStream_t s);
 
 // Scratch of the 8-bit expert sum (forward_int8.cu), for a slice of up to Tcap tokens.

@@ -89,7 +89,8 @@ def check(bffn, x, W, s_w, bias, out_dtype, **kw):
 
 SHAPES = [(1, 4096, 4096), (1, 16, 1), (2, 128, 127), (32, 2048, 8192), (17, 2064, 1007), (333, 2064, 1007),
           (64, 4096, 256), (100, 48, 130), (129, 256, 512), (300, 1024, 3000), (700, 512, 2050), (1000, 8192, 129),
-          (16, 12288, 300), (257, 144, 4100)]
+          (16, 12288, 300), (257, 144, 4100), (2048, 1024, 4096), (4096, 256, 5000), (3001, 272, 2700),
+          (8200, 128, 1100)]
 
 
 @pytest.mark.parametrize("T,K,O", SHAPES)
