@@ -92,6 +92,14 @@ struct IlShared {
 
 __device__ __forceinline__ void il_put(float* y, float v) { *y = v; }
 __device__ __forceinline__ void il_put(__nv_bfloat16* y, float v) { *y = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void il_put4(float* y, const float (&f)[4]) {
+    *reinterpret_cast<float4*>(y) = make_float4(f[0], f[1], f[2], f[3]);
+}
+__device__ __forceinline__ void il_put4(__nv_bfloat16* y, const float (&f)[4]) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+    *reinterpret_cast<uint2*>(y) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
 
 }  // namespace
 
@@ -285,23 +293,48 @@ int8_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
         // (every block of the cluster has the same tile: tiles == clusters)
         cluster_barrier_sync();
         if (warp >= 4 && first < tiles && sh.abort == 0) {
+            // a warp adds a column at a time, a lane four channels of it over the S blocks
             const int to = first % a.tiles_o, tt = first / a.tiles_o;
-            const int q = warp & 3, half = (warp - 4) >> 2, ch = q * 32 + lane;
-            const int t0 = tt * N, o = to * 128 + ch;
-            const float sw = o < a.O ? __ldg(a.sw + o) : 0.f;
-            const float b = (a.bias != nullptr && o < a.O) ? __ldg(a.bias + o) : 0.f;
+            const int t0 = tt * N, o = to * 128 + lane * 4;
+            float sw[4], bs[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                sw[i] = o + i < a.O ? __ldg(a.sw + o + i) : 0.f;
+                bs[i] = a.bias != nullptr && o + i < a.O ? __ldg(a.bias + o + i) : 0.f;
+            }
             OutT* y = static_cast<OutT*>(a.y) + (size_t)t0 * a.O + o;
-            const int c1 = min((N * (rank + 1)) / S, a.T - t0);
+            const int c1 = min(N * (rank + 1) / S, a.T - t0);
+            float st_next = 0.f;
+            int c = N * rank / S + warp - 4;
+            if (c < c1) st_next = __ldcg(a.sx + t0 + c);
 #pragma unroll 1
-            for (int c = (N * rank) / S + half; c < c1; c += 2) {
-                const float st = __ldcg(a.sx + t0 + c);
-                const uint32_t off = smem_u32(smem) + (uint32_t)(c * 128 + ch) * 4u;
-                int u[8], v = 0;
+            for (; c < c1; c += 8) {
+                const float st = st_next;
+                if (c + 8 < c1) st_next = __ldcg(a.sx + t0 + c + 8);
+                const uint32_t off = smem_u32(smem) + (uint32_t)(c * 128 + lane * 4) * 4u;
+                float4 u[8];   // (int32 bits; all blocks' sums in flight at once)
 #pragma unroll
-                for (int r = 0; r < 8; ++r) u[r] = r < S ? ld_shared_cluster_s32(mapa_shared(off, (uint32_t)r)) : 0;
+                for (int r = 0; r < 8; ++r)
+                    u[r] = r < S ? ld_shared_cluster_f4(mapa_shared(off, (uint32_t)r)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                int v[4] = {0, 0, 0, 0};
 #pragma unroll
-                for (int r = 0; r < 8; ++r) v += u[r];
-                if (o < a.O) il_put(y + (size_t)c * a.O, fmaf((float)v * sw, st, b));
+                for (int r = 0; r < 8; ++r) {
+                    v[0] += __float_as_int(u[r].x);
+                    v[1] += __float_as_int(u[r].y);
+                    v[2] += __float_as_int(u[r].z);
+                    v[3] += __float_as_int(u[r].w);
+                }
+                float f[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[i] = fmaf((float)v[i] * sw[i], st, bs[i]);
+                OutT* yc = y + (size_t)c * a.O;
+                if ((a.O & 3) == 0) {   // (rows are then aligned to four values, and whole)
+                    if (o < a.O) il_put4(yc, f);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (o + i < a.O) il_put(yc + i, f[i]);
+                }
             }
         }
         cluster_barrier_sync_relaxed();   // no block leaves while its partial sums may be read
@@ -571,11 +604,11 @@ void int8_linear_plan(int T, int K, int O, int sms, int* N_out, int* S_out, bool
     for (int N = 16; N <= 256; N *= 2) {
         const long long tiles = (long long)tiles_o * ((T + N - 1) / N);
         for (int S = 1; S <= 8; ++S) {
-            if (S > 1 && (N > 64 || tiles > int8_cluster_capacity(S) || KB / S < 2)) continue;
+            if (S > 1 && (N > 128 || tiles > int8_cluster_capacity(S) || KB / S < 2)) continue;
             const double waves = S > 1 ? 1.0 : (double)((tiles + sms - 1) / sms);
             const double mma = 2.0 * N, load = (128.0 + N) * 128.0 / 48.0;
             const double per = (double)((KB + S - 1) / S) * (mma > load ? mma : load);
-            const double cost = waves * (per + N * 4.0) + 1500.0 + (S > 1 ? 1200.0 : 0.0);
+            const double cost = waves * (per + N * 4.0) + 1500.0 + (S > 1 ? 1200.0 + N / S * 80.0 : 0.0);
             if (cost < best) {
                 best = cost;
                 *N_out = N;
