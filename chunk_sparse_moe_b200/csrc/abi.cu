@@ -593,8 +593,9 @@ blockffn_status blockffn_forward_int8(const void* x, const float* gates, const i
         out.lgNB = n <= 16 ? 4 : n <= 32 ? 5 : 6;
         out.S = 1;
         const long long items = (long long)out.slabs * ((n + out.TT - 1) / out.TT);
+        const int* const fit = int8_cluster_capacity();
         for (int S = 2; S <= 8; ++S)
-            if (items <= int8_cluster_capacity(S) && S <= E) out.S = S;
+            if (items <= fit[S] && S <= E) out.S = S;
         out.stages = 0;
         out.wait_ns = in.wait_ns;
         CUtensorMap maps[6];

@@ -1032,7 +1032,8 @@ constexpr int kMaxSmem = 227 * 1024;
 template <int MT>
 cudaError_t launch_in(const X8In& a, const CUtensorMap* maps, int grid, size_t smem, cudaStream_t s) {
     auto kern = int8_experts_in_kernel<MT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    static SmemOptIn opt_in;
+    cudaError_t e = opt_in(kern);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute at[2];
     cudaLaunchConfig_t cfg = x8_config(grid, kXiThreads, smem, s, at, a.CS);
@@ -1061,7 +1062,7 @@ cudaError_t launch_int8_experts_in(X8In a, const CUtensorMap* maps, int sms, cud
     const int MT = a.d_e / 128, stage = MT * kXTile + (128 << a.lgN);
     a.stages = kXRing / stage < kXMaxStages ? kXRing / stage : kXMaxStages;
     const size_t smem = 1024 + (size_t)a.stages * stage + sizeof(XiShared);
-    const int fit = a.CS > 1 ? int8_cluster_capacity(a.CS) * a.CS : sms;
+    const int fit = a.CS > 1 ? int8_cluster_capacity()[a.CS] * a.CS : sms;
     const int grid = fit > 0 ? fit : sms / a.CS * a.CS;
     switch (MT) {
         case 1: return launch_in<1>(a, maps, grid, smem, s);
@@ -1077,7 +1078,8 @@ cudaError_t launch_int8_experts_out(X8Out a, const CUtensorMap* maps, cudaStream
     a.stages = room < kXoMaxStages ? room : kXoMaxStages;
     const size_t smem = 1024 + (size_t)a.stages * stage + (size_t)(a.TT + 1) * 512 + sizeof(XoShared);
     auto kern = int8_experts_out_kernel;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    static SmemOptIn opt_in;
+    cudaError_t e = opt_in(kern);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute at[2];
     cudaLaunchConfig_t cfg = x8_config(a.slabs * a.S, kXoThreads, smem, s, at, a.S);

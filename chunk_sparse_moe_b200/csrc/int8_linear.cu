@@ -539,7 +539,8 @@ template <typename OutT>
 cudaError_t launch_il(const IlArgs& a, const CUtensorMap* maps, int grid, cudaStream_t s) {
     const size_t smem = il_smem(a.stages, a.N);
     auto kern = int8_linear_kernel<OutT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(227 * 1024));
+    static SmemOptIn opt_in;
+    cudaError_t e = opt_in(kern);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
@@ -559,14 +560,14 @@ cudaError_t launch_il(const IlArgs& a, const CUtensorMap* maps, int grid, cudaSt
 }
 }  // namespace
 
-// How many clusters of S blocks of these kernels (one block per SM) can be resident at
+// [S]: how many clusters of S blocks of these kernels (one block per SM) can be resident at
 // once on the current device; 0 if unknown.  (On a B200 that is 148, 74, 45, 33, 26, 22, 15, 15 for
 // S = 1 .. 8: an SM that is left over in its GPC holds no cluster.)
-int int8_cluster_capacity(int S) {
-    static int cache[64][9];
+const int* int8_cluster_capacity() {
+    static int cache[65][9];
     static std::once_flag once[64];
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || S < 1 || S > 8) return 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cache[64];   // all 0
     std::call_once(once[dev], [dev]() {
         auto kern = int8_linear_kernel<float>;
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess) return;
@@ -588,7 +589,7 @@ int int8_cluster_capacity(int S) {
             }
         }
     });
-    return cache[dev][S];
+    return cache[dev];
 }
 
 // Tile width and K split.  A tile of N tokens costs about 2 N cycles of MMA for each
@@ -598,13 +599,14 @@ int int8_cluster_capacity(int S) {
 // Pairs of blocks (tiles of 256 x 256) bring 64 KB for what single blocks' 256 x 256 takes 96.
 void int8_linear_plan(int T, int K, int O, int sms, int* N_out, int* S_out, bool* pair_out) {
     const int KB = (K + 127) / 128, tiles_o = (O + 127) / 128;
+    const int* const fit = int8_cluster_capacity();
     double best = 1e30;
     *N_out = 256;
     *S_out = 1;
     for (int N = 16; N <= 256; N *= 2) {
         const long long tiles = (long long)tiles_o * ((T + N - 1) / N);
         for (int S = 1; S <= 8; ++S) {
-            if (S > 1 && (N > 128 || tiles > int8_cluster_capacity(S) || KB / S < 2)) continue;
+            if (S > 1 && (N > 128 || tiles > fit[S] || KB / S < 2)) continue;
             const double waves = S > 1 ? 1.0 : (double)((tiles + sms - 1) / sms);
             const double mma = 2.0 * N, load = (128.0 + N) * 128.0 / 48.0;
             const double per = (double)((KB + S - 1) / S) * (mma > load ? mma : load);
@@ -616,7 +618,7 @@ void int8_linear_plan(int T, int K, int O, int sms, int* N_out, int* S_out, bool
             }
         }
     }
-    const int pairs = int8_cluster_capacity(2);
+    const int pairs = fit[2];
     *pair_out = false;
     if (pairs > 0) {
         const long long tiles = (long long)((O + 255) / 256) * ((T + 255) / 256);
@@ -634,7 +636,8 @@ namespace {
 template <typename OutT>
 cudaError_t launch_ip(const IlArgs& a, const CUtensorMap* maps, int grid, cudaStream_t s) {
     auto kern = int8_linear_pair_kernel<OutT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    static SmemOptIn opt_in;
+    cudaError_t e = opt_in(kern);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
@@ -652,7 +655,7 @@ cudaError_t launch_ip(const IlArgs& a, const CUtensorMap* maps, int grid, cudaSt
 
 cudaError_t launch_int8_linear(IlArgs a, const CUtensorMap* maps, bool bf16_out, int sms, cudaStream_t s) {
     if (a.pair) {
-        const int tiles = a.tiles_o * a.tiles_t, fit = int8_cluster_capacity(2);
+        const int tiles = a.tiles_o * a.tiles_t, fit = int8_cluster_capacity()[2];
         const int grid = 2 * (tiles < fit ? tiles : fit);
         return bf16_out ? launch_ip<__nv_bfloat16>(a, maps, grid, s) : launch_ip<float>(a, maps, grid, s);
     }

@@ -1,6 +1,7 @@
 // launch.h -- host-side launchers of the BlockFFN kernels (internal to the
 // library; the public interface is include/blockffn.h).
 #pragma once
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -132,6 +133,26 @@ cudaError_t launch_route_topk_backward(const void* logits, bool bf16, const int3
 // rows of K values rounded to 8 bits, one scale per row (int8_linear.cu)
 cudaError_t launch_quantize_rows(const void* v, bool bf16, int rows, int K, int8_t* q, float* scale, cudaStream_t s);
 
+// A kernel's permission to use 227 KB of shared memory, asked for once per device (one
+// static object for each kernel).
+class SmemOptIn {
+  public:
+    template <typename K>
+    cudaError_t operator()(K kern) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const unsigned long long bit = 1ull << (dev & 63);
+        if (done_.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        if (e == cudaSuccess) done_.fetch_or(bit, std::memory_order_relaxed);
+        return e;
+    }
+
+  private:
+    std::atomic<unsigned long long> done_{0};
+};
+
 // Arguments of the 8-bit integer product (int8_linear.cu).
 struct IlArgs {
     const float* sx;          // [T] token scales
@@ -148,7 +169,7 @@ struct IlArgs {
     int kb_lo[9];             // first K block of each of the S blocks (set by the launcher)
     unsigned long long wait_ns;
 };
-int int8_cluster_capacity(int S);
+const int* int8_cluster_capacity();   // [9], by blocks per cluster
 void int8_linear_plan(int T, int K, int O, int sms, int* N, int* S, bool* pair);
 // maps: W [O, K] (box {128, 128}) and q [T, K] (box {128, N}; pair: {128, 128}), bytes, 128-byte swizzle
 cudaError_t launch_int8_linear(IlArgs a, const CUtensorMap* maps, bool bf16_out, int sms, cudaStream_t s);
