@@ -118,10 +118,14 @@ __global__ void __launch_bounds__(kQThreads) int8_prepare_kernel(const __nv_bflo
 }
 
 // --------------------------------------------------------------- experts_in --
-constexpr int kXGather = 4;                  // gathering warps of experts_in: 2, 3, 12, ..
-constexpr int kXiThreads = 384 + 32 * (kXGather - 2);
-constexpr int kXStep = 4 * kXGather;         // token rows they copy at a time
-constexpr int kXRows = 128 / kXStep;
+// Gathering warps of experts_in (2, 3, 12, ..): as many as its registers leave room for.
+template <int MT>
+struct XiCfg {
+    static constexpr int kGather = MT <= 2 ? 8 : 4;
+    static constexpr int kThreads = 384 + 32 * (kGather - 2);
+    static constexpr int kStep = 4 * kGather;         // token rows they copy at a time
+    static constexpr int kRows = 128 / kStep;
+};
 constexpr int kXMaxStages = 10;
 constexpr int kXTile = 128 * 128;            // 128 rows x 128 int8
 constexpr int kXRing = 200 * 1024;
@@ -242,7 +246,7 @@ __device__ __forceinline__ void xi_finish(const X8In& a, XiShared& sh, const int
 }  // namespace
 
 template <int MT>
-__global__ void __launch_bounds__(kXiThreads, 1)
+__global__ void __launch_bounds__(XiCfg<MT>::kThreads, 1)
 int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                        const X8In a) {
     extern __shared__ uint8_t smem_raw[];
@@ -261,7 +265,7 @@ int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_co
     if (threadIdx.x == 0) {
         for (int i = 0; i < a.stages; ++i) {
             mbar_init(&sh.full[i], 1);
-            mbar_init(&sh.gathered[i], a.T <= N ? 1 : kXGather);
+            mbar_init(&sh.gathered[i], a.T <= N ? 1 : XiCfg<MT>::kGather);
             mbar_init(&sh.empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -391,34 +395,47 @@ int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_co
         } else {
         // Gather: eight lanes copy one token row's 128 bytes in 16-byte pieces into the
         // swizzled layout (piece c of row r lies at c ^ (r & 7)); the warps take four rows
-        // each in turn.  The MMA reads the rows through the async proxy, and the fence
-        // that this takes waits for the block's copies in flight, so it is made once for
-        // half a ring of stages.
+        // each in turn.  The MMA reads the rows through the async proxy, and the fence that
+        // this takes waits for the block's copies in flight, so it is made once for a group of
+        // stages; up to two later groups are under way meanwhile.
+        constexpr int kRows = XiCfg<MT>::kRows, kStep = XiCfg<MT>::kStep;
         const int gw = warp < 4 ? warp - 2 : warp - 10;
         const int r0 = gw * 4 + (lane >> 3), c = lane & 7;
         const uint32_t dst0 = (uint32_t)(r0 * 128 + ((c ^ (r0 & 7)) << 4));
-        const int batch = a.stages / 2;
-        int st = 0, ann = 0, pending = 0;
+        const int batch = a.stages >= 6 ? 2 : 1;                              // stages of a group
+        // groups under way behind the oldest when that is awaited: two fewer than the ring has, so
+        // that the MMAs of one and the copies of another do not wait for each other in turn
+        const int later = min(2, a.stages / batch - 2);
+        int st = 0, ann = 0, filled = 0, groups = 0, announced = 0;
+        auto announce = [&]() {   // the oldest group has landed
+            fence_proxy_async_smem();
+            __syncwarp();
+            for (int k = 0; k < batch; ++k) {
+                if (lane == 0) mbar_arrive(&sh.gathered[ann]);
+                if (++ann == a.stages) ann = 0;
+            }
+            ++announced;
+        };
         uint32_t ph = 0;
         bool ok = true;
-        int next[kXRows];   // the next tile's tokens, on their way
+        int next[kRows];   // the next tile's tokens, on their way
         XiItem it = {0, 0, 0};
         auto fetch = [&](int i) {
             if (i >= tiles) return;
             it = xi_item(sh, a.E, i);
             const int32_t* list = a.w.list + (size_t)it.e * a.w.Tcap + it.base;
 #pragma unroll
-            for (int u = 0; u < kXRows; ++u) {
+            for (int u = 0; u < kRows; ++u) {
                 next[u] = 0;
-                if (kXStep * u < it.rows) next[u] = __ldcg(list + min(kXStep * u + r0, it.rows - 1));
+                if (kStep * u < it.rows) next[u] = __ldcg(list + min(kStep * u + r0, it.rows - 1));
             }
         };
         fetch(first);
         for (int i = first; i < tiles && ok; i += step) {
-            uint32_t tok[kXRows];
+            uint32_t tok[kRows];
             const int rows = it.rows;
 #pragma unroll
-            for (int u = 0; u < kXRows; ++u) tok[u] = (uint32_t)next[u] * (uint32_t)a.KB;   // in 128-byte rows
+            for (int u = 0; u < kRows; ++u) tok[u] = (uint32_t)next[u] * (uint32_t)a.KB;   // in 128-byte rows
             fetch(i + step);
             for (int kb = kb0; kb < kb1; ++kb) {
                 ok = wait_bar_warp(&sh.empty[st], ph ^ 1u, limit, &sh.abort, a.ctl, kWaitEmpty);
@@ -426,25 +443,35 @@ int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_co
                 uint8_t* sp = smem + (size_t)st * stage_bytes + a_bytes + dst0;
                 const int8_t* src = a.w.xq + kb * 128 + c * 16;
 #pragma unroll
-                for (int u = 0; u < kXRows; ++u)
-                    if (kXStep * u < rows) cp_async_16(sp + u * kXStep * 128, src + (size_t)tok[u] * 128);
-                ++pending;
+                for (int u = 0; u < kRows; ++u)
+                    if (kStep * u < rows) cp_async_16(sp + u * kStep * 128, src + (size_t)tok[u] * 128);
                 if (++st == a.stages) {
                     st = 0;
                     ph ^= 1u;
                 }
-                if (pending >= batch || (kb == kb1 - 1 && i + step >= tiles)) {
-                    cp_async_wait_all();
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    for (; pending > 0; --pending) {
-                        if (lane == 0) mbar_arrive(&sh.gathered[ann]);
-                        if (++ann == a.stages) ann = 0;
+                if (++filled == batch) {
+                    filled = 0;
+                    ++groups;
+                    cp_async_commit();
+                    if (groups - announced > later) {
+                        if (later == 2) cp_async_wait<2>();
+                        else if (later == 1) cp_async_wait<1>();
+                        else cp_async_wait<0>();
+                        announce();
                     }
                 }
             }
         }
-        cp_async_wait_all();   // (after a timeout: no copy is in flight when the block ends)
+        cp_async_wait_all();
+        while (announced < groups) announce();
+        if (filled > 0) {   // a last group of fewer stages
+            fence_proxy_async_smem();
+            __syncwarp();
+            for (; filled > 0; --filled) {
+                if (lane == 0) mbar_arrive(&sh.gathered[ann]);
+                if (++ann == a.stages) ann = 0;
+            }
+        }
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -512,48 +539,60 @@ int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_co
                     on[w] = __ballot_sync(0xffffffffu, t < a.T && __ldg(a.gates + (size_t)t * a.E + it.e) != 0.f);
                 }
             }
+            // What is known of the group's columns (at most 64: column j of the group is column
+            // 16 (j / 8) + 8 group + j % 8 of the tile) before the sums are there: lane i holds
+            // its columns i and i + 32.
+            int tks[2] = {0, 0}, slots[2] = {-1, -1};
+            float sxs[2] = {0.f, 0.f}, gts[2] = {0.f, 0.f};
+            if (S == 1) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int j = lane + 32 * u, c = 16 * (j >> 3) + 8 * group + (j & 7);
+                    if (c >= width) continue;
+                    if (!dense) {
+                        slots[u] = it.base + c;
+                        tks[u] = __ldcg(a.w.list + pair0 + slots[u]);
+                    } else {
+                        const int w = c >> 5;
+                        const uint32_t word = w == 0 ? on[0] : w == 1 ? on[1] : w == 2 ? on[2] : on[3];
+                        if (!(word >> (c & 31) & 1u)) continue;
+                        tks[u] = c;
+                        slots[u] = __popc(word & ((1u << (c & 31)) - 1u)) + (w > 0 ? __popc(on[0]) : 0) +
+                                   (w > 1 ? __popc(on[1]) : 0) + (w > 2 ? __popc(on[2]) : 0);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    if (slots[u] >= 0) {
+                        sxs[u] = __ldcg(a.w.sx + tks[u]);
+                        gts[u] = __ldg(a.gates + (size_t)tks[u] * a.E + it.e);
+                    }
+            }
             // (the group leaves its loop together)
             if (!bar_all(1 + group, wait_bar_warp(&sh.acc_full[buf], bph, limit, &sh.abort, a.ctl, kWaitAccFull))) break;
             tc_fence_after();
             const uint32_t tacc = tmem + (uint32_t)(buf * MT * N) + ((uint32_t)(q * 32) << 16);
             if (S == 1) {
                 if (group * PW >= width && lane == 0) mbar_arrive(&sh.acc_empty[buf]);   // nothing for this group
-                int tk = 0, slot = -1;
-                float sx = 0.f, gt = 0.f;
-                auto column = [&](int c) {   // what lane i (of PW) knows of column c + i
-                    c += lane & (PW - 1);
-                    slot = -1;
-                    if (c >= width) return;
-                    if (!dense) {
-                        slot = it.base + c;
-                        tk = __ldcg(a.w.list + pair0 + slot);
-                    } else {
-                        const int w = c >> 5;
-                        const uint32_t word = w == 0 ? on[0] : w == 1 ? on[1] : w == 2 ? on[2] : on[3];
-                        if (!(word >> (c & 31) & 1u)) return;
-                        tk = c;
-                        slot = __popc(word & ((1u << (c & 31)) - 1u)) + (w > 0 ? __popc(on[0]) : 0) +
-                               (w > 1 ? __popc(on[1]) : 0) + (w > 2 ? __popc(on[2]) : 0);
-                    }
-                    sx = __ldcg(a.w.sx + tk);
-                    gt = __ldg(a.gates + (size_t)tk * a.E + it.e);
-                };
-                column(group * PW);
 #pragma unroll 1
-                for (int c = group * PW; c < width; c += 2 * PW) {
+                for (int p = 0, c = group * PW; c < width; ++p, c += 2 * PW) {
                     int v[MT][PW];
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) tmem_ld_piece(tacc + (uint32_t)(mt * N + c), v[mt]);
-                    const int tk0 = tk, slot0 = slot;
-                    const float sx0 = sx, gt0 = gt;
-                    column(c + 2 * PW);
+                    // lane i of the piece: the group's column 8 p + i
+                    const int from = (8 * p + (lane & (PW - 1))) & 31;
+                    const bool hi = p >= 4;
+                    const int slot = __shfl_sync(0xffffffffu, hi ? slots[1] : slots[0], from);
+                    const int tk = __shfl_sync(0xffffffffu, hi ? tks[1] : tks[0], from);
+                    const float sx = __shfl_sync(0xffffffffu, hi ? sxs[1] : sxs[0], from);
+                    const float gt = __shfl_sync(0xffffffffu, hi ? gts[1] : gts[0], from);
                     tmem_ld_wait();
                     if (c + 2 * PW >= width) {   // the group's last piece is in registers
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);
                     }
-                    xi_finish<MT, PW>(a, sh, v, pair0, slot0, tk0, sx0, gt0, si, bi, group, q, lane, parity);
+                    xi_finish<MT, PW>(a, sh, v, pair0, slot, tk, sx, gt, si, bi, group, q, lane, parity);
                 }
             } else {
                 // partial sums [column][MT * 128] int32 over the stages (all read)
@@ -1036,7 +1075,7 @@ cudaError_t launch_in(const X8In& a, const CUtensorMap* maps, int grid, size_t s
     cudaError_t e = opt_in(kern);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute at[2];
-    cudaLaunchConfig_t cfg = x8_config(grid, kXiThreads, smem, s, at, a.CS);
+    cudaLaunchConfig_t cfg = x8_config(grid, XiCfg<MT>::kThreads, smem, s, at, a.CS);
     return cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], a);
 }
 
