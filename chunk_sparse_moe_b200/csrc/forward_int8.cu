@@ -366,55 +366,50 @@ int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_co
             }
         }
         __syncwarp();
-    } else if (warp == 2 || warp == 3 || warp >= 12) {
-        if (dense) {
-            if (warp == 2 && elect_one()) {
-                const uint64_t pol = policy_evict_normal();
-                int st = 0, issued = 0;
-                uint32_t ph = 0;
-                bool ok = true;
-                for (int i = first; i < tiles && ok; i += step) {
-                    for (int kb = kb0; kb < kb1; ++kb) {
-                        ok = wait_bar(&sh.empty[st], ph ^ 1u, limit, &sh.abort, a.ctl, kWaitEmpty);
-                        if (!ok) break;
-                        mbar_arrive_expect_tx(&sh.gathered[st], (uint32_t)(N * 128));
-                        tma_load_2d(smem + (size_t)st * stage_bytes + a_bytes, &tm_x, &sh.gathered[st], kb * 128, 0, pol);
-                        ++issued;
-                        if (++st == a.stages) {
-                            st = 0;
-                            ph ^= 1u;
-                        }
+    } else if (dense && (warp == 2 || warp == 3 || warp >= 12)) {
+        if (warp == 2 && elect_one()) {
+            const uint64_t pol = policy_evict_normal();
+            int st = 0, issued = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int i = first; i < tiles && ok; i += step) {
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    ok = wait_bar(&sh.empty[st], ph ^ 1u, limit, &sh.abort, a.ctl, kWaitEmpty);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&sh.gathered[st], (uint32_t)(N * 128));
+                    tma_load_2d(smem + (size_t)st * stage_bytes + a_bytes, &tm_x, &sh.gathered[st], kb * 128, 0, pol);
+                    ++issued;
+                    if (++st == a.stages) {
+                        st = 0;
+                        ph ^= 1u;
                     }
                 }
-                const int in_ring = min(issued, a.stages);
-                for (int i = 0; i < in_ring; ++i) {
-                    st = st == 0 ? a.stages - 1 : st - 1;
-                    wait_bar_drain(&sh.gathered[st], (uint32_t)(((issued - 1 - i) / a.stages) & 1), limit, a.ctl);
-                }
             }
-        } else {
+            const int in_ring = min(issued, a.stages);
+            for (int i = 0; i < in_ring; ++i) {
+                st = st == 0 ? a.stages - 1 : st - 1;
+                wait_bar_drain(&sh.gathered[st], (uint32_t)(((issued - 1 - i) / a.stages) & 1), limit, a.ctl);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 2 || warp == 3 || warp >= 12) {
         // Gather: eight lanes copy one token row's 128 bytes in 16-byte pieces into the
         // swizzled layout (piece c of row r lies at c ^ (r & 7)); the warps take four rows
-        // each in turn.  The MMA reads the rows through the async proxy, and the fence that
-        // this takes waits for the block's copies in flight, so it is made once for a group of
-        // stages; up to two later groups are under way meanwhile.
+        // each in turn.  A stage is announced once it has landed and the two behind it (fewer
+        // in a short ring, which leaves the MMAs and the copies a stage each) are under way; the
+        // MMA reads the rows through the async proxy, hence the fence.
         constexpr int kRows = XiCfg<MT>::kRows, kStep = XiCfg<MT>::kStep;
         const int gw = warp < 4 ? warp - 2 : warp - 10;
         const int r0 = gw * 4 + (lane >> 3), c = lane & 7;
         const uint32_t dst0 = (uint32_t)(r0 * 128 + ((c ^ (r0 & 7)) << 4));
-        const int batch = a.stages >= 6 ? 2 : 1;                              // stages of a group
-        // groups under way behind the oldest when that is awaited: two fewer than the ring has, so
-        // that the MMAs of one and the copies of another do not wait for each other in turn
-        const int later = min(2, a.stages / batch - 2);
-        int st = 0, ann = 0, filled = 0, groups = 0, announced = 0;
-        auto announce = [&]() {   // the oldest group has landed
+        const int later = min(2, a.stages - 2);
+        int st = 0, ann = 0, pending = 0;
+        auto announce = [&]() {   // the oldest stage has landed
             fence_proxy_async_smem();
             __syncwarp();
-            for (int k = 0; k < batch; ++k) {
-                if (lane == 0) mbar_arrive(&sh.gathered[ann]);
-                if (++ann == a.stages) ann = 0;
-            }
-            ++announced;
+            if (lane == 0) mbar_arrive(&sh.gathered[ann]);
+            if (++ann == a.stages) ann = 0;
+            --pending;
         };
         uint32_t ph = 0;
         bool ok = true;
@@ -449,30 +444,17 @@ int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_co
                     st = 0;
                     ph ^= 1u;
                 }
-                if (++filled == batch) {
-                    filled = 0;
-                    ++groups;
-                    cp_async_commit();
-                    if (groups - announced > later) {
-                        if (later == 2) cp_async_wait<2>();
-                        else if (later == 1) cp_async_wait<1>();
-                        else cp_async_wait<0>();
-                        announce();
-                    }
+                cp_async_commit();
+                if (++pending > later) {
+                    if (later == 2) cp_async_wait<2>();
+                    else if (later == 1) cp_async_wait<1>();
+                    else cp_async_wait<0>();
+                    announce();
                 }
             }
         }
         cp_async_wait_all();
-        while (announced < groups) announce();
-        if (filled > 0) {   // a last group of fewer stages
-            fence_proxy_async_smem();
-            __syncwarp();
-            for (; filled > 0; --filled) {
-                if (lane == 0) mbar_arrive(&sh.gathered[ann]);
-                if (++ann == a.stages) ann = 0;
-            }
-        }
-        }
+        while (pending > 0) announce();
         __syncwarp();
     } else if (warp == 1) {
         const uint64_t desc0 = sw128_kmajor_desc(smem_u32(smem));
