@@ -146,6 +146,20 @@ bool make_map_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t oute
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same tensor (inner a multiple of 128) as blocks of 128 columns: a box is two of them,
+// landing as two [box_outer x 128 B] swizzled tiles (a block behind the last is zeros).
+bool make_map_u8_pair(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint32_t box_outer) {
+    auto fn = encode_fn();
+    if (fn == nullptr) return false;
+    cuuint64_t dims[3] = {128, outer, inner / 128};
+    cuuint64_t strides[2] = {inner, 128};
+    cuuint32_t box[3] = {128, box_outer, 2};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Which kernel computes a forward call.
 enum class Path { F32, Decode, Group };
 
@@ -455,15 +469,19 @@ blockffn_status blockffn_int8_linear(const void* x, blockffn_dtype dt, const int
     a.ctl = reinterpret_cast<Ctl*>(ws);
     a.T = T;
     a.O = O;
-    a.KB = (K + 127) / 128;
     int8_linear_plan(T, K, O, G, &a.N, &a.S, &a.pair);
+    a.KP = K % 128 == 0 && K >= 256 && a.N <= 128 && !a.pair ? 2 : 1;   // (three stages or more)
+    a.KB = (K + 128 * a.KP - 1) / (128 * a.KP);
     a.tiles_o = a.pair ? (O + 255) / 256 : (O + 127) / 128;
     a.tiles_t = (T + a.N - 1) / a.N;
     a.stages = 0;
     a.wait_ns = g_wait_ns.load();
     CUtensorMap maps[2];
-    if (!make_map_u8(&maps[0], W, (uint64_t)K, (uint64_t)O, 128) ||
-        !make_map_u8(&maps[1], q, (uint64_t)K, (uint64_t)T, a.pair ? 128u : (uint32_t)a.N))
+    const uint32_t rows = a.pair ? 128u : (uint32_t)a.N;
+    if (a.KP == 2 ? !make_map_u8_pair(&maps[0], W, (uint64_t)K, (uint64_t)O, 128) ||
+                        !make_map_u8_pair(&maps[1], q, (uint64_t)K, (uint64_t)T, rows)
+                  : !make_map_u8(&maps[0], W, (uint64_t)K, (uint64_t)O, 128) ||
+                        !make_map_u8(&maps[1], q, (uint64_t)K, (uint64_t)T, rows))
         return fail(BLOCKFFN_ERR_CUDA, "cuTensorMapEncodeTiled failed");
     cudaError_t e = launch_quantize_rows(x, dt == BLOCKFFN_BF16, T, K, q, sx, s);
     if (e != cudaSuccess) return cuda_fail(e, "quantize launch");

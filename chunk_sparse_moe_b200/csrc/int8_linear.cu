@@ -10,9 +10,11 @@
 //
 // Tiles.  128 output channels (M, the weight's rows) by N tokens (N = 16 .. 256):
 // the weight is the operand that a small batch streams, so it fills the MMA's M
-// whatever T is.  A pipeline stage is 128 bytes of K of both operands, brought by
-// TMA in the 128-byte swizzle the MMA reads; K's tail and the rows behind O and T
-// are zeros that TMA fills in.
+// whatever T is.  A pipeline stage is 128 bytes of K of both operands, or 256 (KP = 2)
+// where K is whole 128-byte blocks: a TMA operation takes an SM's TMA unit about
+// 0.15-0.27 us whatever it brings up to 32 KB, so fewer and larger ones.  TMA writes the
+// 128-byte swizzle the MMA reads; K's tail and the rows behind O and T are zeros that it
+// fills in.
 //
 // Few tiles: a cluster of S blocks shares a tile, each multiplying a slice of K.  The
 // int32 partial sums stay in each block's shared memory; after a cluster barrier
@@ -103,14 +105,22 @@ __device__ __forceinline__ void il_put4(__nv_bfloat16* y, const float (&f)[4]) {
 
 }  // namespace
 
-template <typename OutT>
+// A stage's operand: KP blocks of 128 bytes of K of `rows` rows, one TMA operation.
+template <int KP>
+__device__ __forceinline__ void il_load(void* dst, const CUtensorMap* m, uint64_t* bar, int kb, int row, uint64_t pol) {
+    if constexpr (KP == 1) tma_load_2d(dst, m, bar, kb * 128, row, pol);
+    else tma_load_3d(dst, m, bar, 0, row, kb * KP, pol);
+}
+
+template <typename OutT, int KP>
 __global__ void __launch_bounds__(kIlThreads, 1)
 int8_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                    const __grid_constant__ IlArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int N = a.N, S = a.S;
-    const int stage_bytes = kIlABytes + N * 128;
+    constexpr int kA = KP * kIlABytes;
+    const int b_tile = N * 128, stage_bytes = kA + KP * b_tile;
     IlShared& sh = *reinterpret_cast<IlShared*>(smem + (size_t)a.stages * stage_bytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = S > 1 ? (int)cluster_ctarank() : 0;
@@ -159,7 +169,7 @@ int8_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
                 pre = min(a.stages, kb1 - kb0);
                 for (int i = 0; i < pre; ++i) {
                     mbar_arrive_expect_tx(&sh.full[i], (uint32_t)stage_bytes);
-                    tma_load_2d(smem + (size_t)i * stage_bytes, &tm_w, &sh.full[i], (kb0 + i) * 128, to * 128, pol);
+                    il_load<KP>(smem + (size_t)i * stage_bytes, &tm_w, &sh.full[i], kb0 + i, to * 128, pol);
                 }
             }
             griddep_wait();
@@ -175,9 +185,9 @@ int8_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
                             break;
                         }
                         mbar_arrive_expect_tx(&sh.full[st], (uint32_t)stage_bytes);
-                        tma_load_2d(sp, &tm_w, &sh.full[st], kb * 128, to * 128, pol);
+                        il_load<KP>(sp, &tm_w, &sh.full[st], kb, to * 128, pol);
                     }
-                    tma_load_2d(sp + kIlABytes, &tm_x, &sh.full[st], kb * 128, tt * N, pol);
+                    il_load<KP>(sp + kA, &tm_x, &sh.full[st], kb, tt * N, pol);
                     ++issued;
                     if (++st == a.stages) {
                         st = 0;
@@ -210,10 +220,13 @@ int8_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t ad = desc0 + (uint64_t)((uint32_t)st * (uint32_t)stage_bytes >> 4);
-                    const uint64_t bd = ad + (kIlABytes >> 4);
+                    const uint64_t bd = ad + (kA >> 4);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        umma_i8(tmem + (uint32_t)(buf * N), ad + 2 * k, bd + 2 * k, idesc, kb > kb0 || k > 0);
+                    for (int h = 0; h < KP; ++h)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            umma_i8(tmem + (uint32_t)(buf * N), ad + h * (kIlABytes >> 4) + 2 * k,
+                                    bd + (uint64_t)(h * (b_tile >> 4)) + 2 * k, idesc, kb > kb0 || h + k > 0);
                     umma_commit(&sh.empty[st]);
                     if (kb == kb1 - 1) umma_commit(&sh.acc_full[buf]);
                     if (++st == a.stages) {
@@ -349,7 +362,8 @@ int8_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
 // that takes a single block 48 KB, and has its 128 channels of all 256 tokens in its own
 // TMEM.  L2's delivery is what bounds the single-block form (about 55 bytes a cycle and SM).
 // The pair's first block issues the MMAs; the loads of both blocks are counted on its
-// barriers, and finished MMAs are reported to both.
+// barriers, and finished MMAs are reported to both.  (Stages of 256 bytes of K, as above,
+// measured 61.4 us against 60.1 with the rounding at 4096^3: three long stages for six.)
 namespace {
 
 constexpr int kIpStages = 6;
@@ -372,7 +386,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kIlThreads, 1)
 int8_linear_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                         const __grid_constant__ IlArgs a) {
     constexpr int N = 256;
-    extern __shared__ uint8_t smem_raw[];
+        extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     IpShared& sh = *reinterpret_cast<IpShared*>(smem + kIpStages * kIpStage);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -533,12 +547,12 @@ int8_linear_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_c
 }
 
 namespace {
-size_t il_smem(int stages, int N) { return 1024 + (size_t)stages * (kIlABytes + N * 128) + sizeof(IlShared); }
+size_t il_smem(const IlArgs& a) { return 1024 + (size_t)a.stages * a.KP * (kIlABytes + a.N * 128) + sizeof(IlShared); }
 
-template <typename OutT>
+template <typename OutT, int KP>
 cudaError_t launch_il(const IlArgs& a, const CUtensorMap* maps, int grid, cudaStream_t s) {
-    const size_t smem = il_smem(a.stages, a.N);
-    auto kern = int8_linear_kernel<OutT>;
+    const size_t smem = il_smem(a);
+    auto kern = int8_linear_kernel<OutT, KP>;
     static SmemOptIn opt_in;
     cudaError_t e = opt_in(kern);
     if (e != cudaSuccess) return e;
@@ -569,7 +583,7 @@ const int* int8_cluster_capacity() {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cache[64];   // all 0
     std::call_once(once[dev], [dev]() {
-        auto kern = int8_linear_kernel<float>;
+        auto kern = int8_linear_kernel<float, 1>;
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess) return;
         for (int c = 1; c <= 8; ++c) {
             cudaLaunchAttribute at[1];
@@ -659,12 +673,14 @@ cudaError_t launch_int8_linear(IlArgs a, const CUtensorMap* maps, bool bf16_out,
         const int grid = 2 * (tiles < fit ? tiles : fit);
         return bf16_out ? launch_ip<__nv_bfloat16>(a, maps, grid, s) : launch_ip<float>(a, maps, grid, s);
     }
-    const int stage = kIlABytes + a.N * 128;
+    const int stage = a.KP * (kIlABytes + a.N * 128);
     a.stages = kIlRing / stage < kIlMaxStages ? kIlRing / stage : kIlMaxStages;
     const int tiles = a.tiles_o * a.tiles_t;
     for (int r = 0; r <= a.S; ++r) a.kb_lo[r] = (int)((long long)a.KB * r / a.S);
     const int grid = a.S > 1 ? tiles * a.S : (tiles < sms ? tiles : sms);
-    return bf16_out ? launch_il<__nv_bfloat16>(a, maps, grid, s) : launch_il<float>(a, maps, grid, s);
+    if (a.KP == 2)
+        return bf16_out ? launch_il<__nv_bfloat16, 2>(a, maps, grid, s) : launch_il<float, 2>(a, maps, grid, s);
+    return bf16_out ? launch_il<__nv_bfloat16, 1>(a, maps, grid, s) : launch_il<float, 1>(a, maps, grid, s);
 }
 
 }  // namespace bffn

@@ -161,7 +161,8 @@ struct IlArgs {
     void* y;                  // [T, O]
     Ctl* ctl;
     int T, O;
-    int KB;                   // 128-byte blocks of K
+    int KP;                   // 128-byte blocks of K in a pipeline stage (1 or 2)
+    int KB;                   // stages that K takes
     int N, S;                 // tokens per tile, blocks per tile (K split)
     bool pair;                // pairs of blocks, tiles of 256 x 256 (cta_group::2)
     int tiles_o, tiles_t;
@@ -171,7 +172,8 @@ struct IlArgs {
 };
 const int* int8_cluster_capacity();   // [9], by blocks per cluster
 void int8_linear_plan(int T, int K, int O, int sms, int* N, int* S, bool* pair);
-// maps: W [O, K] (box {128, 128}) and q [T, K] (box {128, N}; pair: {128, 128}), bytes, 128-byte swizzle
+// maps: W [O, K] (box {128, 128}) and q [T, K] (box {128, N}; pair: {128, 128}), bytes, 128-byte swizzle;
+// KP = 2: as blocks of 128 columns, boxes of two
 cudaError_t launch_int8_linear(IlArgs a, const CUtensorMap* maps, bool bf16_out, int sms, cudaStream_t s);
 
 // Scratch of the 8-bit expert sum (forward_int8.cu), for a slice of up to Tcap tokens.
