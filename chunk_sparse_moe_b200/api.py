@@ -221,6 +221,11 @@ def _want(t: torch.Tensor, what: str, dtype, shape, device) -> torch.Tensor:
     return t
 
 
+def _same_device(workspace: "Workspace", device: torch.device) -> None:
+    if workspace.buf.device != device:
+        raise ValueError(f"workspace: on {workspace.buf.device}, expected {device}")
+
+
 def _launch(where: str, fn, device: torch.device, *args) -> None:
     """Call ``fn(*args, stream)`` with the tensors' device current, on its current stream."""
     if device.index == torch.cuda.current_device():
@@ -291,6 +296,8 @@ def quantize_int8(w: torch.Tensor):
         raise ValueError(f"w: shape {tuple(w.shape)} has no rows to round")
     cols = w.shape[-1]
     rows = w.numel() // cols
+    if rows >= 2 ** 31 or cols >= 2 ** 31:
+        raise ValueError(f"w: shape {tuple(w.shape)} has too many rows or columns")
     q = torch.empty(w.shape, dtype=torch.int8, device=w.device)
     scale = torch.empty(w.shape[:-1], dtype=torch.float32, device=w.device)
     _launch("blockffn_quantize_int8", lib.blockffn_quantize_int8, w.device, _ptr(w), rows, cols, _dtype_code(w),
@@ -318,6 +325,7 @@ def int8_linear(x: torch.Tensor, W: torch.Tensor, s_w: torch.Tensor, bias: Optio
         _want(y, "y", out_dtype or y.dtype, (T, O), dev)
     if workspace is None:
         workspace = Workspace.for_int8_linear(T, K, O, dev)
+    _same_device(workspace, dev)
     _launch("blockffn_int8_linear", lib.blockffn_int8_linear, dev, _ptr(x), _dtype_code(x), _ptr(W), _ptr(s_w),
             _ptr(bias), T, K, O, _dtype_code(y), _ptr(y), _ptr(workspace.buf), workspace.nbytes)
     return y
@@ -358,6 +366,7 @@ def forward_int8(x: torch.Tensor, gates: torch.Tensor, W_in: torch.Tensor, s_in:
         _want(y, "y", x.dtype, (T, d_h), dev)
     if workspace is None:
         workspace = Workspace.for_forward_int8(T, d_h, E, d_e, dev)
+    _same_device(workspace, dev)
     _launch("blockffn_forward_int8", lib.blockffn_forward_int8, dev, _ptr(x), _ptr(gates), _ptr(W_in), _ptr(s_in),
             _ptr(W_out), _ptr(s_out), T, d_h, E, d_e, _dtype_code(x), opts, _ptr(y), _ptr(workspace.buf),
             workspace.nbytes)

@@ -404,7 +404,7 @@ blockffn_status blockffn_quantize_int8(const void* w, int rows, int cols, blockf
     if (!w || !q || !scale) return fail(BLOCKFFN_ERR_INVALID_ARG, "null pointer");
     if (!aligned16(w) || !aligned16(q) || !aligned16(scale))
         return fail(BLOCKFFN_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
-    cudaError_t e = launch_quantize_rows(w, dt == BLOCKFFN_BF16, rows, cols, q, scale,
+    cudaError_t e = launch_quantize_rows(w, dt == BLOCKFFN_BF16, rows, cols, q, scale, nullptr,
                                          static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? BLOCKFFN_OK : cuda_fail(e, "quantize_int8 launch");
 }
@@ -483,7 +483,7 @@ blockffn_status blockffn_int8_linear(const void* x, blockffn_dtype dt, const int
                   : !make_map_u8(&maps[0], W, (uint64_t)K, (uint64_t)O, 128) ||
                         !make_map_u8(&maps[1], q, (uint64_t)K, (uint64_t)T, rows))
         return fail(BLOCKFFN_ERR_CUDA, "cuTensorMapEncodeTiled failed");
-    cudaError_t e = launch_quantize_rows(x, dt == BLOCKFFN_BF16, T, K, q, sx, s);
+    cudaError_t e = launch_quantize_rows(x, dt == BLOCKFFN_BF16, T, K, q, sx, a.ctl, s);
     if (e != cudaSuccess) return cuda_fail(e, "quantize launch");
     e = launch_int8_linear(a, maps, y_dt == BLOCKFFN_BF16, G, s);
     return e == cudaSuccess ? BLOCKFFN_OK : cuda_fail(e, "int8_linear launch");
@@ -580,7 +580,7 @@ blockffn_status blockffn_forward_int8(const void* x, const float* gates, const i
         const __nv_bfloat16* xs = static_cast<const __nv_bfloat16*>(x) + (size_t)t0 * d_h;
         const float* gs = gates + (size_t)t0 * E;
         w.C32 = (n + 31) / 32;
-        cudaError_t e = launch_int8_prepare(xs, gs, n, d_h, E, w, s);
+        cudaError_t e = launch_int8_prepare(xs, gs, n, d_h, E, w, ctl, s);
         if (e != cudaSuccess) return cuda_fail(e, "8-bit prepare launch");
         X8In in;
         in.w = w;

@@ -20,17 +20,26 @@
 //   experts_in : tiles of one expert x up to N of its tokens, all of d_e.  Up to 64 tokens
 //                are all multiplied (what counts is the weights' bytes); else x rows are
 //                gathered in 16-byte asynchronous copies straight into the MMA's
-//                swizzled layout (two warps; TMA's gather of four rows an operation took
-//                about 60 cycles each, 18 us for a tile of 128 rows at d_h 2048).  The tile holds whole rows of h, so the epilogue finds
-//                their scales and writes 8-bit h.  Few tiles: a cluster's blocks
-//                split d_h and add their int32 sums through distributed shared memory.
+//                swizzled layout (TMA's gather of four rows an operation took about 60
+//                cycles each, 18 us for a tile of 128 rows at d_h 2048).  The tile holds whole rows of h, so the epilogue finds their scales and
+//                writes 8-bit h.  Few tiles: a cluster's blocks split d_h and add their int32
+//                sums through distributed shared memory.
 //   experts_out: a block owns TT consecutive tokens x 128 output channels as fp32
 //                sums in shared memory and walks the experts; a token tile's tokens
 //                are neighbours in every expert's list, so h comes in plain boxes of
-//                16 rows.  Each int32 result column is scaled and added to its
+//                16, 32 or 64 rows.  Each int32 result column is scaled and added to its
 //                token's row.  Few tiles: a cluster's blocks share the experts and
 //                add their fp32 rows in rank order.
 // The three kernels are programmatic dependents of one another.
+//
+// What bounds them.  Decode: the way through three dependent launches, each with a plan
+// to read (14 us for one token, 18 us for a 32-token chunk, where 8-bit weights take 2.6 to
+// 3.5 us to read).  Long inputs (112 us at 4096 tokens, 8 of 64 experts, d_h 2048): in
+// experts_out the sums' read-modify-write in shared memory, 8 bytes for every pair and
+// channel (57 % of the shared-memory pipe, 6 % of the tensor pipe, 80 us under a
+// profiler, 1.73 waves of blocks).  Tried there and slower: entries in twos under
+// one barrier with their pieces pipelined (118 -> 123 us), four epilogue groups instead
+// of two (118 -> 123 us), 128-token tiles (142 -> 198 us: twice the entries).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -48,17 +57,18 @@ constexpr int kPrepBatch = 16;   // gates a thread has in flight
 template <int C>
 __global__ void __launch_bounds__(kQThreads) int8_prepare_kernel(const __nv_bfloat16* __restrict__ x,
                                                                  const float* __restrict__ gates, int T, int d_h,
-                                                                 int E, int lgW, const X8Bufs w) {
+                                                                 int E, int lgW, const X8Bufs w, Ctl* ctl) {
     constexpr int kWarps = kQThreads / 32;
     __shared__ uint32_t red[kPrepBatch * kWarps + 1];
     griddep_wait();
     griddep_launch_dependents();
+    const Int8Gate gate = int8_gate(ctl);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if ((int)blockIdx.x >= E) {
         const int W = 1 << lgW, g = tid >> lgW, t = (((int)blockIdx.x - E) << (8 - lgW)) + g;
         if (t < T)
             quantize_row<__nv_bfloat16, C>(x + (size_t)t * d_h, d_h, w.xq + (size_t)t * d_h, w.sx + t, W, tid & (W - 1),
-                                           1 + g, red + (g << lgW >> 5));
+                                           1 + g, red + (g << lgW >> 5), gate);
         return;
     }
     const int e = blockIdx.x;
@@ -77,7 +87,7 @@ __global__ void __launch_bounds__(kQThreads) int8_prepare_kernel(const __nv_bflo
             on[i] = __ballot_sync(0xffffffffu, __uint_as_float(on[i]) != 0.f);
             if (lane == 0) red[i * kWarps + warp] = (uint32_t)__popc(on[i]);
         }
-        __syncthreads();
+        if (!__syncthreads_and(int8_gate_open(gate))) return;
         if (warp == 0) {   // running sums over the batch's warps, in token order
             constexpr int kPer = kPrepBatch * kWarps / 32;
             uint32_t c[kPer], s = 0;
@@ -139,6 +149,7 @@ struct XiShared {
     uint64_t mma_done;
     uint32_t tmem_base;
     volatile int abort;
+    int refused;                             // an earlier error, written once, before the first barrier
     uint32_t colmax[2][2][4][16];            // by warp group, piece parity, warp
     int cnt[256];
     int per[256];                            // tokens of each of an expert's tiles
@@ -311,6 +322,7 @@ int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_co
         }
         if (lane == 0) {
             sh.first[a.E] = run;
+            sh.refused = status != 0;
             if (status != 0) sh.abort = 1;
         }
     }
@@ -319,7 +331,7 @@ int8_experts_in_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_co
     tc_fence_after();
     const uint32_t tmem = sh.tmem_base;
     const uint64_t limit = a.wait_ns;
-    const int all = sh.first[a.E], tiles = sh.abort ? 0 : all;
+    const int all = sh.first[a.E], tiles = sh.refused ? 0 : all;
 
     // A slice of at most N tokens is not gathered: column c of every tile is token c, all
     // of them are multiplied, and the epilogue takes the columns of the expert's tokens.
@@ -692,6 +704,7 @@ struct alignas(16) XoShared {
     uint64_t mma_done;
     uint32_t tmem_base;
     volatile int abort;
+    int refused;                             // an earlier error, written once, before the first barrier
     int n_ent;
     uint32_t ent[kXoMaxEnt];                 // expert << 24 | (pairs - 1) << 16 | first pair in its list
     XoMeta meta[kXoAcc];
@@ -774,7 +787,8 @@ int8_experts_out_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_c
         for (int i = 0; i < 8; ++i) {
             const int e = 32 * i + lane;
             lo[i] = hi[i] = 0;
-            if (e < a.E) {
+            // (after an earlier error the tables may be another call's: no entries then)
+            if (e < a.E && status == 0) {
                 lo[i] = __ldcg(a.w.tpos + (size_t)e * (a.w.C32 + 1) + c0);
                 hi[i] = __ldcg(a.w.tpos + (size_t)e * (a.w.C32 + 1) + c1);
             }
@@ -799,6 +813,7 @@ int8_experts_out_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_c
         }
         if (lane == 0) {
             sh.n_ent = run;
+            sh.refused = status != 0;
             if (status != 0) sh.abort = 1;
         }
     }
@@ -807,7 +822,7 @@ int8_experts_out_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_c
     tc_fence_after();
     const uint32_t tmem = sh.tmem_base;
     const uint64_t limit = a.wait_ns;
-    const int ents = sh.abort ? 0 : sh.n_ent;
+    const int ents = sh.n_ent;
     // this block's share (at most 1024 entries: fp32 quotients are exact)
     const float per_rank = __fdividef(1.f, (float)S);
     const int m0 = (int)(((float)(ents * rank) + 0.25f) * per_rank);
@@ -1064,15 +1079,15 @@ cudaError_t launch_in(const X8In& a, const CUtensorMap* maps, int grid, size_t s
 }  // namespace
 
 cudaError_t launch_int8_prepare(const __nv_bfloat16* x, const float* gates, int T, int d_h, int E, const X8Bufs& w,
-                                cudaStream_t s) {
+                                Ctl* ctl, cudaStream_t s) {
     const QuantPlan p = quantize_plan(T, d_h, 2);
     const int per = kQThreads >> p.lgW;
     cudaLaunchAttribute at[2];
     cudaLaunchConfig_t cfg = x8_config(E + (T + per - 1) / per, kQThreads, 0, s, at, 1);
-    if (p.C == 0) return cudaLaunchKernelEx(&cfg, int8_prepare_kernel<0>, x, gates, T, d_h, E, p.lgW, w);
-    if (p.C == 2) return cudaLaunchKernelEx(&cfg, int8_prepare_kernel<2>, x, gates, T, d_h, E, p.lgW, w);
-    if (p.C == 4) return cudaLaunchKernelEx(&cfg, int8_prepare_kernel<4>, x, gates, T, d_h, E, p.lgW, w);
-    return cudaLaunchKernelEx(&cfg, int8_prepare_kernel<8>, x, gates, T, d_h, E, p.lgW, w);
+    if (p.C == 0) return cudaLaunchKernelEx(&cfg, int8_prepare_kernel<0>, x, gates, T, d_h, E, p.lgW, w, ctl);
+    if (p.C == 2) return cudaLaunchKernelEx(&cfg, int8_prepare_kernel<2>, x, gates, T, d_h, E, p.lgW, w, ctl);
+    if (p.C == 4) return cudaLaunchKernelEx(&cfg, int8_prepare_kernel<4>, x, gates, T, d_h, E, p.lgW, w, ctl);
+    return cudaLaunchKernelEx(&cfg, int8_prepare_kernel<8>, x, gates, T, d_h, E, p.lgW, w, ctl);
 }
 
 // Tokens per tile and blocks per cluster.  A tile of all an expert's tokens reads its

@@ -82,6 +82,41 @@ __device__ __forceinline__ int ld_shared_cluster_s32(uint32_t cluster_addr) {
     return v;
 }
 
+// --------------------------------------------------------------- workspace --
+// The 8-bit calls keep nothing in a workspace but its status word, so they share one
+// freely among themselves; one that a forward call keeps its counters in is not theirs (and
+// a forward refuses one of theirs in the same way: its shape key differs).
+constexpr unsigned long long kInt8Key = 0x3862697473ull | 1ull;
+
+// What a thread of a call's first kernel reads of the control block at its start, so that
+// the read runs beside its inputs' (waited for alone it cost a decode call 0.4 us).
+struct Int8Gate {
+    Ctl* ctl;    // nullptr: a call without a workspace
+    int32_t status;
+    unsigned long long key;
+};
+__device__ __forceinline__ Int8Gate int8_gate(Ctl* ctl) {
+    Int8Gate g{ctl, 0, kInt8Key};
+    if (ctl != nullptr) {
+        g.status = __ldcg(&ctl->status);
+        g.key = __ldcg(&ctl->shape_key);
+    }
+    return g;
+}
+// May this thread write?  Not after an earlier error, nor into a forward's workspace, which
+// is recorded.  Threads may read the status while a dependent kernel records a wait that
+// ran out, so they need not agree: no barrier follows, or the block decides together.
+__device__ __forceinline__ bool int8_gate_open(const Int8Gate& g) {
+    if (g.status != 0) return false;
+    if (g.key == kInt8Key) return true;
+    if (g.key == 0) {
+        if (threadIdx.x == 0) claim_shape_key(g.ctl, kInt8Key);
+        return true;
+    }
+    if (threadIdx.x == 0) record_error(g.ctl, kErrWorkspace, kShapeKey);
+    return false;
+}
+
 // ------------------------------------------------- 8-bit rounding of a row --
 // q = rint(127 v / amax), scale = amax / 127.  A row that is all zero (or below
 // 2^-120, where 127 / amax would overflow) has q = 0 and scale 0; a row with an
@@ -197,7 +232,7 @@ __device__ __forceinline__ uint2 quantize_chunk(const uint4& u, const RowScale& 
 // K, two passes.  red: a word per warp of the group.
 template <typename T, int C>
 __device__ __forceinline__ void quantize_row(const T* __restrict__ v, int K, int8_t* __restrict__ q, float* scale, int W,
-                                             int t, int bar, uint32_t* red) {
+                                             int t, int bar, uint32_t* red, const Int8Gate& gate) {
     constexpr int V = 16 / (int)sizeof(T);
     uint4 u[C > 0 ? C : 1];
     uint32_t m = 0;
@@ -219,6 +254,7 @@ __device__ __forceinline__ void quantize_row(const T* __restrict__ v, int K, int
         named_bar_sync(bar, W);
         for (int w = 0; w < W / 32; ++w) m = max(m, red[w]);
     }
+    if (!int8_gate_open(gate)) return;   // (behind the last barrier)
     const RowScale r = row_scale(m);
     if (t == 0) *scale = r.scale;
     if constexpr (C > 0) {

@@ -39,19 +39,22 @@ namespace bffn {
 
 template <typename T, int C>
 __global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(const T* __restrict__ v, int rows, int K, int lgW,
-                                                                  int8_t* __restrict__ q, float* __restrict__ scale) {
+                                                                  int8_t* __restrict__ q, float* __restrict__ scale,
+                                                                  Ctl* ctl) {
     __shared__ uint32_t red[8];
     griddep_wait();
     griddep_launch_dependents();
+    const Int8Gate gate = int8_gate(ctl);
     const int W = 1 << lgW, g = threadIdx.x >> lgW;   // the block's group of W threads
     const long long row = ((long long)blockIdx.x << (8 - lgW)) + g;
     if (row >= rows) return;
-    quantize_row<T, C>(v + row * K, K, q + row * K, scale + row, W, threadIdx.x & (W - 1), 1 + g, red + (g << lgW >> 5));
+    quantize_row<T, C>(v + row * K, K, q + row * K, scale + row, W, threadIdx.x & (W - 1), 1 + g, red + (g << lgW >> 5),
+                       gate);
 }
 
 namespace {
 template <typename T>
-cudaError_t launch_quantize_t(const T* v, int rows, int K, int8_t* q, float* scale, cudaStream_t s) {
+cudaError_t launch_quantize_t(const T* v, int rows, int K, int8_t* q, float* scale, Ctl* ctl, cudaStream_t s) {
     const QuantPlan p = quantize_plan(rows, K, (int)sizeof(T));
     const int per = kQThreads >> p.lgW;
     cudaLaunchConfig_t cfg = {};
@@ -63,16 +66,17 @@ cudaError_t launch_quantize_t(const T* v, int rows, int K, int8_t* q, float* sca
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (p.C == 0) return cudaLaunchKernelEx(&cfg, quantize_rows_kernel<T, 0>, v, rows, K, p.lgW, q, scale);
-    if (p.C == 2) return cudaLaunchKernelEx(&cfg, quantize_rows_kernel<T, 2>, v, rows, K, p.lgW, q, scale);
-    if (p.C == 4) return cudaLaunchKernelEx(&cfg, quantize_rows_kernel<T, 4>, v, rows, K, p.lgW, q, scale);
-    return cudaLaunchKernelEx(&cfg, quantize_rows_kernel<T, 8>, v, rows, K, p.lgW, q, scale);
+    if (p.C == 0) return cudaLaunchKernelEx(&cfg, quantize_rows_kernel<T, 0>, v, rows, K, p.lgW, q, scale, ctl);
+    if (p.C == 2) return cudaLaunchKernelEx(&cfg, quantize_rows_kernel<T, 2>, v, rows, K, p.lgW, q, scale, ctl);
+    if (p.C == 4) return cudaLaunchKernelEx(&cfg, quantize_rows_kernel<T, 4>, v, rows, K, p.lgW, q, scale, ctl);
+    return cudaLaunchKernelEx(&cfg, quantize_rows_kernel<T, 8>, v, rows, K, p.lgW, q, scale, ctl);
 }
 }  // namespace
 
-cudaError_t launch_quantize_rows(const void* v, bool bf16, int rows, int K, int8_t* q, float* scale, cudaStream_t s) {
-    return bf16 ? launch_quantize_t(static_cast<const __nv_bfloat16*>(v), rows, K, q, scale, s)
-                : launch_quantize_t(static_cast<const float*>(v), rows, K, q, scale, s);
+cudaError_t launch_quantize_rows(const void* v, bool bf16, int rows, int K, int8_t* q, float* scale, Ctl* ctl,
+                                 cudaStream_t s) {
+    return bf16 ? launch_quantize_t(static_cast<const __nv_bfloat16*>(v), rows, K, q, scale, ctl, s)
+                : launch_quantize_t(static_cast<const float*>(v), rows, K, q, scale, ctl, s);
 }
 
 namespace {

@@ -130,8 +130,10 @@ cudaError_t launch_route_topk_backward(const void* logits, bool bf16, const int3
                                        int E, int k, bool sigmoid, bool renorm, float scale, void* d_logits,
                                        cudaStream_t s);
 
-// rows of K values rounded to 8 bits, one scale per row (int8_linear.cu)
-cudaError_t launch_quantize_rows(const void* v, bool bf16, int rows, int K, int8_t* q, float* scale, cudaStream_t s);
+// rows of K values rounded to 8 bits, one scale per row (int8_linear.cu); ctl: the control
+// block of the workspace that q and scale are in, or nullptr
+cudaError_t launch_quantize_rows(const void* v, bool bf16, int rows, int K, int8_t* q, float* scale, Ctl* ctl,
+                                 cudaStream_t s);
 
 // A kernel's permission to use 227 KB of shared memory, asked for once per device (one
 // static object for each kernel).
@@ -189,7 +191,7 @@ struct X8Bufs {
     int C32;                  // ceil(T / 32) of the slice
 };
 cudaError_t launch_int8_prepare(const __nv_bfloat16* x, const float* gates, int T, int d_h, int E, const X8Bufs& w,
-                                cudaStream_t s);
+                                Ctl* ctl, cudaStream_t s);
 
 struct X8In {
     X8Bufs w;

@@ -205,9 +205,10 @@ blockffn_status blockffn_quantize_int8(const void* w, int rows, int cols, blockf
  * A token with an infinity or NaN gives a row of NaN.
  * workspace: ws_bytes >= blockffn_int8_linear_workspace_bytes(T, K, O) (0 for shapes
  * that are refused), reset once before its first use; it holds nothing between
- * calls but the status word, so calls of any shapes may share one that is large
- * enough, as long as they cannot overlap on the GPU.  After a device-side error the
- * outputs of that call are undefined.
+ * calls but the status word, so 8-bit calls of any shapes may share one that is large
+ * enough, as long as they cannot overlap on the GPU; not one that blockffn_forward uses
+ * (see blockffn_forward_int8).  After a device-side error the outputs of that call are
+ * undefined, and later calls compute nothing until the workspace is reset.
  * Requirements: T >= 0, O >= 1, K >= 16 a multiple of 16, K <= 131056.
  */
 size_t blockffn_int8_linear_workspace_bytes(int T, int K, int O);
@@ -336,14 +337,18 @@ blockffn_status blockffn_forward(const void* x, const float* gates, const void* 
  * x, y [T, d_h] bf16 (dt must be BLOCKFFN_BF16); gates [T, E] fp32; W_in [E, d_e, d_h]
  * and W_out [E, d_h, d_e] int8 with channel scales s_in [E, d_e] and s_out [E, d_h]
  * fp32; opts as in blockffn_forward.  y is fully overwritten (zeros for a token with no
- * active expert, before a LayerNorm); a token that holds an infinity or NaN, or an
- * active gate that is one, gives a row of NaN and touches no other row.
+ * active expert, before a LayerNorm); it may be x itself when there is no LayerNorm.  A
+ * token that holds an infinity or NaN, or an active gate that is one, gives a row that is
+ * not finite and touches no other row.
  * workspace: ws_bytes >= blockffn_forward_int8_workspace_bytes(T, d_h, E, d_e) (0 for
  * shapes that are refused), reset once before its first use; it holds nothing between
- * calls but the status word, so calls of any shapes may share one that is large
- * enough, as long as they cannot overlap on the GPU.  Inputs above 8192 tokens run in
- * slices of that many.  After a device-side error the outputs of that call are
- * undefined and later calls compute nothing until the workspace is reset.
+ * calls but the status word, so 8-bit calls of any shapes may share one that is large
+ * enough, as long as they cannot overlap on the GPU.  A workspace that blockffn_forward
+ * has used is refused until it is reset, and the other way round
+ * (blockffn_get_device_status: BLOCKFFN_ERR_WORKSPACE, detail 10; nothing is computed).
+ * Inputs above 8192 tokens run in slices of that many.  After a device-side error the
+ * outputs of that call are undefined and later calls compute nothing until the workspace
+ * is reset.
  * Requirements: T >= 0, 1 <= E <= 256, d_h % 128 == 0, d_e in {128, 256, 384, 512}.
  */
 size_t blockffn_forward_int8_workspace_bytes(int T, int d_h, int E, int d_e);

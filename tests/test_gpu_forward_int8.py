@@ -242,3 +242,88 @@ def test_empty_and_refusals():
             bffn.forward_int8(*[bad if j == i else v for j, v in enumerate(c)])
     with pytest.raises(ValueError):
         bffn.forward_int8(*c, b_in=torch.zeros(4, 1, device="cuda"))
+
+
+def test_workspaces_of_the_two_forms_are_kept_apart():
+    """A workspace that the bf16 forward has used is refused by the 8-bit calls, and the other way round:
+    recorded in its status word, outputs left as they were, usable again after a reset."""
+    bffn = require_cuda()
+    T, d_h, E, d_e = 8, 256, 8, 128
+    d = make(T, d_h, E, d_e, 2, 0.5)
+    c = [d[0].cuda()] + [torch.from_numpy(a).cuda() for a in d[1:6]]
+    W = torch.randint(-127, 128, (64, d_h), device="cuda", dtype=torch.int8)
+    s_w = torch.rand(64, device="cuda")
+    size = max(bffn.Workspace.for_forward_int8(T, d_h, E, d_e).nbytes, bffn.Workspace.for_int8_linear(T, d_h, 64).nbytes,
+               bffn.workspace_bytes(T, d_h, E, d_e, 32, torch.bfloat16, False))
+    wide = [(c[2].float() * c[3][..., None]).bfloat16(), (c[4].float() * c[5][..., None]).bfloat16()]
+    calls = {"forward": lambda ws, y: bffn.forward(c[0], *wide, 32, gates=c[1], y=y, workspace=ws),
+             "forward_int8": lambda ws, y: bffn.forward_int8(*c, y=y, workspace=ws),
+             "int8_linear": lambda ws, y: bffn.int8_linear(c[0], W, s_w, y=y[:, :64].contiguous(), workspace=ws)}
+    for first, second in (("forward", "forward_int8"), ("forward", "int8_linear"), ("forward_int8", "forward"),
+                          ("int8_linear", "forward")):
+        ws = bffn.Workspace(size)
+        y = torch.empty_like(c[0])
+        good = calls[second](bffn.Workspace(size), y.clone())
+        calls[first](ws, y.clone())
+        assert bffn.device_status(ws) == (0, 0)
+        left = calls[second](ws, torch.full_like(y, 9.0))
+        assert bffn.device_status(ws) == (5, 10) and torch.all(left == 9)
+        ws.reset()
+        assert torch.equal(calls[second](ws, y.clone()), good) and bffn.device_status(ws) == (0, 0)
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose first call of each operator is a captured one: nothing that a first call looks up
+    breaks the capture."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch, chunk_sparse_moe_b200 as bffn
+x = torch.randn(32, 256, device='cuda').bfloat16(); z = torch.randn(32, 8, device='cuda')
+W = torch.randint(-127, 128, (64, 256), device='cuda', dtype=torch.int8); s = torch.rand(64, device='cuda')
+qi = torch.randint(-127, 128, (8, 128, 256), device='cuda', dtype=torch.int8); si = torch.rand(8, 128, device='cuda') / 1e3
+qo = torch.randint(-127, 128, (8, 256, 128), device='cuda', dtype=torch.int8); so = torch.rand(8, 256, device='cuda') / 1e3
+w1, w2 = bffn.Workspace(1 << 22), bffn.Workspace(1 << 22)
+def step():
+    y = bffn.int8_linear(x, W, s, workspace=w1)
+    g, i, w = bffn.route_topk(z, 2)
+    d = bffn.route_topk_backward(z, i, w)
+    return y, g, d, bffn.forward_int8(x, g, qi, si, qo, so, workspace=w2)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = step()
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, step()))
+assert bffn.device_status(w1) == (0, 0) and bffn.device_status(w2) == (0, 0)
+print("captured")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+def test_refused_call_reads_no_tables():
+    """A refused call goes by none of the tables in its workspace, whatever they hold: nothing is computed,
+    the outputs stay, and a reset makes the workspace usable."""
+    bffn = require_cuda()
+    for T, d_h, E, d_e in ((5, 256, 8, 128), (64, 256, 64, 256), (700, 256, 16, 128)):
+        d = make(T, d_h, E, d_e, 3, 0.3)
+        c = [d[0].cuda()] + [torch.from_numpy(a).cuda() for a in d[1:6]]
+        size = max(bffn.Workspace.for_forward_int8(T, d_h, E, d_e).nbytes,
+                   bffn.workspace_bytes(T, d_h, E, d_e, 32, torch.bfloat16, False))
+        ws = bffn.Workspace(size)
+        good = bffn.forward_int8(*c, workspace=ws)
+        ws.reset()
+        wide = [(c[2].float() * c[3][..., None]).bfloat16(), (c[4].float() * c[5][..., None]).bfloat16()]
+        bffn.forward(c[0], *wide, 32, gates=c[1], workspace=ws)   # (the workspace is this call's now)
+        assert bffn.device_status(ws) == (0, 0)
+        gen = torch.Generator(device="cuda").manual_seed(T)
+        tables = ws.buf.view(torch.uint8)[256:]   # (behind the control block)
+        tables.random_(0, 256, generator=gen)
+        y = bffn.forward_int8(*c, y=torch.full_like(c[0], 9.0), workspace=ws)
+        assert bffn.device_status(ws) == (5, 10) and torch.all(y == 9)
+        ws.reset()
+        assert torch.equal(bffn.forward_int8(*c, workspace=ws), good)
