@@ -21,9 +21,10 @@
 //                are all multiplied (what counts is the weights' bytes); else x rows are
 //                gathered in 16-byte asynchronous copies straight into the MMA's
 //                swizzled layout (TMA's gather of four rows an operation took about 60
-//                cycles each, 18 us for a tile of 128 rows at d_h 2048).  The tile holds whole rows of h, so the epilogue finds their scales and
-//                writes 8-bit h.  Few tiles: a cluster's blocks split d_h and add their int32
-//                sums through distributed shared memory.
+//                cycles each, 18 us for a tile of 128 rows at d_h 2048).  The tile holds
+//                whole rows of h, so the epilogue finds their scales and writes 8-bit h.
+//                Few tiles: a cluster's blocks split d_h and add their int32 sums through
+//                distributed shared memory.
 //   experts_out: a block owns TT consecutive tokens x 128 output channels as fp32
 //                sums in shared memory and walks the experts; a token tile's tokens
 //                are neighbours in every expert's list, so h comes in plain boxes of
@@ -33,11 +34,12 @@
 // The three kernels are programmatic dependents of one another.
 //
 // What bounds them.  Decode: the way through three dependent launches, each with a plan
-// to read (14 us for one token, 18 us for a 32-token chunk, where 8-bit weights take 2.6 to
-// 3.5 us to read).  Long inputs (112 us at 4096 tokens, 8 of 64 experts, d_h 2048): in
+// to read: at d_h 2048, 8 of 64 experts, 15 us for one token and 19.5 us for a 32-token
+// chunk, whose bytes take 0.7 and 3.4 us.  Long inputs (114 us at 4096 tokens; the three
+// kernels alone 11, 31 and 80 us, the bytes and the products 10.6 us each): in
 // experts_out the sums' read-modify-write in shared memory, 8 bytes for every pair and
-// channel (57 % of the shared-memory pipe, 6 % of the tensor pipe, 80 us under a
-// profiler, 1.73 waves of blocks).  Tried there and slower: entries in twos under
+// channel (57 % of the shared-memory pipe, 6 % of the tensor pipe, 1.73 waves
+// of blocks).  Tried there and slower: entries in twos under
 // one barrier with their pieces pipelined (118 -> 123 us), four epilogue groups instead
 // of two (118 -> 123 us), 128-token tiles (142 -> 198 us: twice the entries).
 #include <cuda.h>

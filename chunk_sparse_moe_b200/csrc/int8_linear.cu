@@ -14,7 +14,7 @@
 // where K is whole 128-byte blocks: a TMA operation takes an SM's TMA unit about
 // 0.15-0.27 us whatever it brings up to 32 KB, so fewer and larger ones.  TMA writes the
 // 128-byte swizzle the MMA reads; K's tail and the rows behind O and T are zeros that it
-// fills in.
+// fills in.  (K = O = 4096: one token 8.0 -> 7.1 us with 256 bytes, weights 2.6 us.)
 //
 // Few tiles: a cluster of S blocks shares a tile, each multiplying a slice of K.  The
 // int32 partial sums stay in each block's shared memory; after a cluster barrier
@@ -368,6 +368,8 @@ int8_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
 // The pair's first block issues the MMAs; the loads of both blocks are counted on its
 // barriers, and finished MMAs are reported to both.  (Stages of 256 bytes of K, as above,
 // measured 61.4 us against 60.1 with the rounding at 4096^3: three long stages for six.)
+// 4096^3: the product alone 55 us (floor 42), the tensor pipe 61 % busy, 686 MB from L2;
+// with the rounding 62 us in a burst, 71 us where the power cap holds the clock at 1680 MHz.
 namespace {
 
 constexpr int kIpStages = 6;

@@ -24,8 +24,11 @@
 // The renormalised weights are formed relative to the largest chosen logit: no
 // sum of theirs underflows, however low the chosen logits are.
 //
-// Bound: reading the logits and writing the gates, T * E * (2 or 4) + T * E * 4
-// bytes; for many experts the instructions of the choice come close to that time.
+// Bound: reading the logits and writing the gates, T * E * (2 or 4) + T * E * 4 bytes, is
+// the floor (10.6 us at 32749 tokens x 256 fp32 logits); the instructions of the choice take
+// longer: 45 us there, 8 of 256 experts in 4 of 8 groups, 76 % of the issue slots
+// (51 us before keys named their expert, 88 us with groups compared one by one).
+// The gradient reads the logits and writes as many: 8.0 us at 16381 x 256 fp32, floor 5.3.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
