@@ -213,10 +213,34 @@ __device__ __forceinline__ void tmem_ld_piece(uint32_t taddr, int (&v)[8]) {
     tmem_ld_32x32b_x8(taddr, reinterpret_cast<uint32_t (&)[8]>(v));
 }
 
+// Swish, z / (1 + exp(-z)): expf (within 2 steps of fp32), the sum rounded once, and the quotient
+// by a reciprocal and one step of refinement with the remainder, which leaves it within half a
+// step and 2^-20 of one.  No branches, so a piece's columns run through it side by side.
+// (Divisor and quotient are carried as d / 8 and 8 h: the reciprocal takes no divisor above
+// 2^126, z below -87.  Below -88.7 exp(-z) is infinite and h -0; an infinite or NaN z gives NaN.)
+__device__ __forceinline__ float xi_swish(float z) {
+    const float d = fmaf(expf(-z), 0.125f, 0.125f);
+    const float r = __fdividef(1.f, d), q = z * r;
+    return d < INFINITY ? fmaf(fmaf(-q, d, z), r, q) * 0.125f : q;
+}
+
+// The whole number q next to 127 h / amax put right where it may be the one on the other side of
+// a border: 127 h - q amax is exact in 64 bits (31 bits each), so what comes out is rint of the
+// exact quotient.
+__device__ __noinline__ float xi_border(float h, float amax, float q) {
+    const double d = 127.0 * (double)h - (double)q * (double)amax, half = 0.5 * (double)amax;
+    if (fabs(d) > half || (fabs(d) == half && ((int)q & 1))) q += d > 0.0 ? 1.f : -1.f;
+    return q;
+}
+
 // What the epilogue does with PW columns (tokens) of int32 sums: h, its scale over all of
 // d_e (the four warps of the group meet in colmax), 8-bit h and the pair's factors.  Lane i
 // (of PW) holds column i's token, its scale and gate, and the place of the pair in the
 // expert's list (slot, -1: no pair); pair0: the list's first pair.
+// z and Swish go to fp32's last bit or two, and the rounding to 8 bits is decided again near the
+// border of two whole numbers: a value on the wrong side moves its token's whole row of y.
+// (From the approximate exponential and quotient alone that was one value in 700000, and h
+// was 0 below z = -87.)
 template <int MT, int PW>
 __device__ __forceinline__ void xi_finish(const X8In& a, XiShared& sh, const int (&v)[MT][PW], size_t pair0, int slot,
                                           int token, float sx, float gate, const float (&si)[MT],
@@ -229,8 +253,8 @@ __device__ __forceinline__ void xi_finish(const X8In& a, XiShared& sh, const int
         uint32_t m = 0;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-            const float z = fmaf((float)v[mt][i] * si[mt], s, bi[mt]);
-            h[mt][i] = __fdividef(z, 1.f + __expf(-z));
+            const float z = __fadd_rn(__fmul_rn((float)v[mt][i] * si[mt], s), bi[mt]);
+            h[mt][i] = xi_swish(z);
             m = max(m, __float_as_uint(h[mt][i]) & 0x7fffffffu);
         }
         m = __reduce_max_sync(0xffffffffu, m);
@@ -245,13 +269,36 @@ __device__ __forceinline__ void xi_finish(const X8In& a, XiShared& sh, const int
     if (q == 0 && lane < PW && slot >= 0)
         a.w.pair[pair0 + slot] = make_float4(__int_as_float(token), gate * r.scale, gate, 0.f);
     int8_t* out = a.w.hq + pair0 * a.d_e + q * 32 + lane;
+    // rounded by adding 1.5 * 2^23 (the whole number is the sum's low byte); what was rounded off
+    // is off by 127 * 2^-24 at most, inv's share
+    constexpr float kMagic = 12582912.f, kNear = 0.49998f;
+    float worst = 0.f;
 #pragma unroll
     for (int i = 0; i < PW; ++i) {
         const float inv = __shfl_sync(0xffffffffu, r.inv, i);
         const int at = __shfl_sync(0xffffffffu, slot, i);
         if (at >= 0) {
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) out[(size_t)at * a.d_e + mt * 128] = (int8_t)(int)rintf(h[mt][i] * inv);
+            for (int mt = 0; mt < MT; ++mt) {
+                const float t = fmaf(h[mt][i], inv, kMagic);
+                worst = fmaxf(worst, fabsf(fmaf(h[mt][i], inv, kMagic - t)));
+                out[(size_t)at * a.d_e + mt * 128] = (int8_t)__float_as_uint(t);
+            }
+        }
+    }
+    if (__any_sync(0xffffffffu, worst > kNear)) {   // (one piece in a hundred)
+#pragma unroll
+        for (int i = 0; i < PW; ++i) {
+            const float inv = __shfl_sync(0xffffffffu, r.inv, i), amax = __shfl_sync(0xffffffffu, r.amax, i);
+            const int at = __shfl_sync(0xffffffffu, slot, i);
+            if (at >= 0) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    const float t = fmaf(h[mt][i], inv, kMagic);
+                    if (fabsf(fmaf(h[mt][i], inv, kMagic - t)) > kNear)
+                        out[(size_t)at * a.d_e + mt * 128] = (int8_t)(int)xi_border(h[mt][i], amax, t - kMagic);
+                }
+            }
         }
     }
 }

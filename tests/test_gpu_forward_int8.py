@@ -327,3 +327,40 @@ def test_refused_call_reads_no_tables():
         assert bffn.device_status(ws) == (5, 10) and torch.all(y == 9)
         ws.reset()
         assert torch.equal(bffn.forward_int8(*c, workspace=ws), good)
+
+
+@pytest.mark.parametrize("shift", [0.0, -20.0, -60.0, -86.0])
+@pytest.mark.parametrize("T", [20, 2048])
+def test_h_is_rounded_as_the_formula_says(T, shift):
+    """The 8-bit h themselves, read through a W_out of ones on the diagonal, at values of z from everyday ones to
+    those where Swish is next to nothing.  The steps of z are IEEE fp32 and repeated here; then expf is off by 2
+    steps (4 U) at most, 1 + e and the quotient by U each, the row's largest value likewise: 127 (6 + 6) U of a
+    step, and everything further from a border between two whole numbers has to be on its side."""
+    bffn = require_cuda()
+    d_h = d_e = 128
+    E, U = 4, 2.0 ** -24
+    rng = np.random.default_rng(int(-shift) + T)
+    x = torch.from_numpy(rng.standard_normal((T, d_h)).astype(np.float32)).to(torch.bfloat16)
+    W_in = rng.integers(-127, 128, (E, d_e, d_h)).astype(np.int8)
+    s_in = ((0.5 + rng.random((E, d_e))) / 73 / np.sqrt(d_h) * (0.3 if shift else 1.0)).astype(np.float32)
+    b_in = (shift + 0.1 * rng.standard_normal((E, d_e))).astype(np.float32)
+    W_out = np.broadcast_to(np.eye(d_h, d_e, dtype=np.int8), (E, d_h, d_e)).copy()
+    s_out = np.ones((E, d_h), np.float32)
+    pick = rng.integers(0, E, T)
+    g = np.zeros((T, E), np.float32)
+    g[np.arange(T), pick] = 1
+    y = call(bffn, (x, g, W_in, s_in, W_out, s_out, b_in, None)).double().cpu().numpy()
+    # z in fp32, as the formula reads
+    xq, _ = quantized(x.double().numpy())
+    sx = (np.abs(x.float().numpy()).max(1) / np.float32(127)).astype(np.float32)
+    v = np.einsum("tk,tjk->tj", xq, W_in[pick].astype(np.float64)).astype(np.float32)   # (below 2^24: exact)
+    z = (v * s_in[pick]) * sx[:, None] + b_in[pick]
+    assert z.dtype == np.float32 and np.abs(v).max() < 2 ** 24
+    h = z.astype(np.float64) / (1 + np.exp(-z.astype(np.float64)))
+    amax = np.abs(h).max(1, keepdims=True)
+    # (below z = -88.7 exp(-z) passes the range of fp32 and h is 0; amax below 2^-120 counts as a row of zeros)
+    assert z.min() > -88.7 and np.all(amax > 1.01 * 2.0 ** -120)
+    # y = hq amax / 127, rounded to bf16: off by 127 * 2^-9 = a quarter of a step at most
+    hq = np.rint(y * 127 / amax)
+    assert np.all(np.abs(hq) <= 127) and np.all(np.abs(np.abs(hq).max(1)) == 127)
+    assert np.all(np.abs(hq - 127 * h / amax) <= 0.5 + 127 * 12.1 * U)
