@@ -183,6 +183,13 @@ __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+// The arriving side of such a barrier (the warp does not wait): its shared-memory writes are
+// seen by the warps that wait there.
+__device__ __forceinline__ void named_bar_arrive(int id, int nthreads) {
+    __syncwarp();
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
 __host__ __device__ inline long long ceil_div_ll(long long a, long long b) {
     return (a + b - 1) / b;
 }

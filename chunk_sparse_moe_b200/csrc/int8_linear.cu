@@ -94,7 +94,10 @@ struct IlShared {
     uint64_t mma_done;
     uint32_t tmem_base;
     volatile int abort;
+    int refused;                          // an earlier error: written once, read behind named barrier 1
 };
+// warp 0 arrives there, the MMA warp and the epilogue wait: the block goes on, or does not, as one
+constexpr int kIlAgree = 32 * (1 + 1 + 8);
 
 __device__ __forceinline__ void il_put(float* y, float v) { *y = v; }
 __device__ __forceinline__ void il_put(__nv_bfloat16* y, float v) { *y = __float2bfloat16_rn(v); }
@@ -159,32 +162,38 @@ int8_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
     const uint32_t tmem = sh.tmem_base;
     const uint64_t limit = a.wait_ns;
 
+    bool refused = false;
+
     if (warp == 0) {
+        // the first stages' weight tiles do not depend on the quantize kernel
+        const int pre = first < tiles ? min(a.stages, kb1 - kb0) : 0;
         // (elect.sync, not lane 0: what one elected lane runs is issued at twice the rate)
+        if (elect_one()) {
+            const uint64_t pol = policy_evict_normal();
+            const int to = first % a.tiles_o;
+            for (int i = 0; i < pre; ++i) {
+                mbar_arrive_expect_tx(&sh.full[i], (uint32_t)stage_bytes);
+                il_load<KP>(smem + (size_t)i * stage_bytes, &tm_w, &sh.full[i], kb0 + i, to * 128, pol);
+            }
+        }
+        __syncwarp();
+        griddep_wait();
+        refused = __shfl_sync(0xffffffffu, __ldcg(&a.ctl->status), 0) != 0;
+        if (lane == 0) sh.refused = refused;
+        named_bar_arrive(1, kIlAgree);
         if (elect_one()) {
             const uint64_t pol = policy_evict_normal();
             int st = 0;
             uint32_t ph = 0;
             bool stop = false;
-            // the first stages' weight tiles do not depend on the quantize kernel
-            int pre = 0;
-            if (first < tiles) {
-                const int to = first % a.tiles_o;
-                pre = min(a.stages, kb1 - kb0);
-                for (int i = 0; i < pre; ++i) {
-                    mbar_arrive_expect_tx(&sh.full[i], (uint32_t)stage_bytes);
-                    il_load<KP>(smem + (size_t)i * stage_bytes, &tm_w, &sh.full[i], kb0 + i, to * 128, pol);
-                }
-            }
-            griddep_wait();
-            if (__ldcg(&a.ctl->status) != 0) sh.abort = 1;   // (the loads begun are still completed)
             int issued = 0;
             for (int tile = first; tile < tiles && !stop; tile += step) {
                 const int to = tile % a.tiles_o, tt = tile / a.tiles_o;
                 for (int kb = kb0; kb < kb1; ++kb) {
                     uint8_t* sp = smem + (size_t)st * stage_bytes;
                     if (issued >= pre) {
-                        if (!wait_bar(&sh.empty[st], ph ^ 1u, limit, &sh.abort, a.ctl, kWaitEmpty)) {
+                        // (refused: the stages begun are still completed, nobody reads them)
+                        if (refused || !wait_bar(&sh.empty[st], ph ^ 1u, limit, &sh.abort, a.ctl, kWaitEmpty)) {
                             stop = true;
                             break;
                         }
@@ -211,10 +220,12 @@ int8_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
     } else if (warp == 1) {
         const uint32_t idesc = idesc_i8_s32(128, N);
         const uint64_t desc0 = sw128_kmajor_desc(smem_u32(smem));
+        named_bar_sync(1, kIlAgree);
+        refused = sh.refused != 0;
         if (elect_one()) {
             int st = 0, buf = 0;
             uint32_t ph = 0, bph = 0;
-            bool ok = true;
+            bool ok = !refused;
             for (int tile = first; tile < tiles && ok; tile += step) {
                 ok = wait_bar(&sh.acc_empty[buf], bph ^ 1u, limit, &sh.abort, a.ctl, kWaitAccEmpty);
                 if (!ok) break;
@@ -248,10 +259,12 @@ int8_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
         __syncwarp();
     } else if (warp >= 4) {
         griddep_wait();   // the token scales
+        named_bar_sync(1, kIlAgree);
+        refused = sh.refused != 0;
         const int q = warp & 3, half = (warp - 4) >> 2, ch = q * 32 + lane;
         int buf = 0;
         uint32_t bph = 0;
-        for (int tile = first; tile < tiles; tile += step) {
+        for (int tile = first; tile < tiles && !refused; tile += step) {
             const int to = tile % a.tiles_o, tt = tile / a.tiles_o;
             const int t0 = tt * N, o = to * 128 + ch;
             // lanes 0-15 hold the token scales of a piece's columns
@@ -309,7 +322,7 @@ int8_linear_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
     if (S > 1) {
         // (every block of the cluster has the same tile: tiles == clusters)
         cluster_barrier_sync();
-        if (warp >= 4 && first < tiles && sh.abort == 0) {
+        if (warp >= 4 && first < tiles && !refused && sh.abort == 0) {
             // a warp adds a column at a time, a lane four channels of it over the S blocks
             const int to = first % a.tiles_o, tt = first / a.tiles_o;
             const int t0 = tt * N, o = to * 128 + lane * 4;
@@ -392,7 +405,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kIlThreads, 1)
 int8_linear_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                         const __grid_constant__ IlArgs a) {
     constexpr int N = 256;
-        extern __shared__ uint8_t smem_raw[];
+    extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     IpShared& sh = *reinterpret_cast<IpShared*>(smem + kIpStages * kIpStage);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -430,7 +443,7 @@ int8_linear_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_c
             uint32_t ph = 0;
             bool ok = true;
             griddep_wait();
-            if (__ldcg(&a.ctl->status) != 0) {
+            if (__ldcg(&a.ctl->status) != 0) {   // an earlier error: no loads, so no sums and no y
                 sh.abort = 1;
                 ok = false;
             }
@@ -463,7 +476,7 @@ int8_linear_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_c
             }
             // after a timeout the blocks may have stopped at different stages, and loads of the
             // second one that the first does not expect cannot be waited for: give them time
-            if (sh.abort) {
+            if (sh.abort && issued > 0) {
                 const uint64_t t0 = globaltimer_ns();
                 while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
             }

@@ -222,3 +222,29 @@ def test_linear_empty_and_refusals():
         bffn.int8_linear(x, W, s_w, y=torch.zeros(4, 7, device="cuda"))
     with pytest.raises(ValueError):
         bffn.quantize_int8(torch.zeros(4, 64, device="cuda").t())
+
+
+@pytest.mark.parametrize("T,K,O", [(8, 256, 64), (1, 4096, 4096), (17, 2064, 1007), (700, 512, 2050), (4096, 128, 1100),
+                                   (8200, 128, 1100), (2048, 1024, 4096)])
+def test_refused_calls_leave_y(T, K, O):
+    """In a workspace that holds an earlier error, or that a bf16 forward uses, nothing is computed whatever form
+    the product takes: one block a tile, clusters that split K, several tiles a block, pairs of blocks."""
+    bffn = require_cuda()
+    x = values((T, K), torch.bfloat16, 1).cuda()
+    W = torch.from_numpy(np.random.default_rng(2).integers(-127, 128, (O, K)).astype(np.int8)).cuda()
+    s_w = torch.rand(O).cuda()
+    ws = bffn.Workspace.for_int8_linear(T, K, O)
+    good = bffn.int8_linear(x, W, s_w, workspace=ws)       # (q and the scales of this call stay behind)
+    torch.cuda.synchronize()
+    ws.buf[:8] = torch.tensor([4, 0, 0, 0, 6, 0, 0, 0], dtype=torch.uint8)   # a wait that ran out
+    y = torch.full_like(good, 9.0)
+    for _ in range(20):
+        bffn.int8_linear(x, W, s_w, y=y, workspace=ws)
+    assert bffn.device_status(ws) == (4, 6) and torch.all(y == 9)
+    ws.reset()
+    ws.buf[24] = 1                                        # (the key of another form's shapes)
+    for _ in range(20):
+        bffn.int8_linear(x, W, s_w, y=y, workspace=ws)
+    assert bffn.device_status(ws) == (5, 10) and torch.all(y == 9)
+    ws.reset()
+    assert torch.equal(bffn.int8_linear(x, W, s_w, workspace=ws), good) and bffn.device_status(ws) == (0, 0)
