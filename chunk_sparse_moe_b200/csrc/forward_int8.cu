@@ -861,9 +861,8 @@ int8_experts_out_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_c
             run += __shfl_sync(0xffffffffu, inc, 31);
         }
         if (lane == 0) {
-            sh.n_ent = run;
+            sh.n_ent = run;   // (0 after an earlier error)
             sh.refused = status != 0;
-            if (status != 0) sh.abort = 1;
         }
     }
     tc_fence_before();
@@ -1058,7 +1057,7 @@ int8_experts_out_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_c
     // y: the blocks of the cluster add their rows in rank order, each its share of the tokens
     if (S > 1) cluster_barrier_sync();
     else __syncthreads();
-    if (sh.abort == 0) {
+    if (!sh.refused && sh.abort == 0) {
         // (a thread four channels of a row)
         const int ra = (int)(((float)(TT * rank) + 0.25f) * per_rank);
         const int rb = min((int)(((float)(TT * (rank + 1)) + 0.25f) * per_rank), a.T - t0);

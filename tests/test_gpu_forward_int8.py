@@ -364,3 +364,25 @@ def test_h_is_rounded_as_the_formula_says(T, shift):
     hq = np.rint(y * 127 / amax)
     assert np.all(np.abs(hq) <= 127) and np.all(np.abs(np.abs(hq).max(1)) == 127)
     assert np.all(np.abs(hq - 127 * h / amax) <= 0.5 + 127 * 12.1 * U)
+
+
+REFUSED = [(1, 256, 16, 128), (32, 2048, 64, 128), (200, 512, 8, 256), (2000, 256, 16, 128), (8192 + 40, 128, 4, 128)]
+
+
+@pytest.mark.parametrize("T,d_h,E,d_e", REFUSED)
+def test_calls_after_an_error_leave_y(T, d_h, E, d_e):
+    """A workspace that holds an earlier error: every form of the last step (clusters that share a tile, one block,
+    several tiles, slices) leaves y as it is, call after call."""
+    bffn = require_cuda()
+    d = make(T, d_h, E, d_e, 5, 0.3)
+    c = [d[0].cuda()] + [torch.from_numpy(a).cuda() for a in d[1:6]]
+    ws = bffn.Workspace.for_forward_int8(T, d_h, E, d_e)
+    good = bffn.forward_int8(*c, workspace=ws)             # (its tables and h stay behind)
+    torch.cuda.synchronize()
+    ws.buf[:8] = torch.tensor([4, 0, 0, 0, 6, 0, 0, 0], dtype=torch.uint8)   # a wait that ran out
+    y = torch.full_like(good, 9.0)
+    for _ in range(20):
+        bffn.forward_int8(*c, y=y, workspace=ws)
+    assert bffn.device_status(ws) == (4, 6) and torch.all(y == 9)
+    ws.reset()
+    assert torch.equal(bffn.forward_int8(*c, workspace=ws), good) and bffn.device_status(ws) == (0, 0)
