@@ -630,7 +630,7 @@ blockffn_status blockffn_forward_int8(const void* x, const float* gates, const i
         if (e != cudaSuccess) return cuda_fail(e, "8-bit experts-out launch");
     }
     if (ln_w) {
-        cudaError_t e = launch_residual_layernorm(y, x, ln_w, ln_b, ln_eps, T, d_h, true, y, s);
+        cudaError_t e = launch_residual_layernorm(y, x, ln_w, ln_b, ln_eps, T, d_h, true, y, s, ctl);
         if (e != cudaSuccess) return cuda_fail(e, "residual layernorm launch");
     }
     return BLOCKFFN_OK;

@@ -14,6 +14,9 @@
 // Launched as a programmatic dependent of the previous kernel on the stream (the
 // forward that produced y): it waits for that kernel before reading anything.
 // Rows that fit the registers take the one-pass variant below.
+// ctl: the control block of the call that y comes from, or nullptr; after an error recorded there
+// y is left as it is.  (Nothing else runs on that workspace meanwhile, so every thread reads the
+// same status; the read runs beside the row's.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -46,10 +49,11 @@ __device__ __forceinline__ float ln_block_sum(float v, float* red) {
 template <typename T>
 __global__ void __launch_bounds__(kLnThreads) residual_layernorm_kernel(
     const T* __restrict__ y, const T* __restrict__ x, const float* __restrict__ ln_gamma,
-    const float* __restrict__ ln_beta, float eps, int d_h, T* out) {
+    const float* __restrict__ ln_beta, float eps, int d_h, T* out, const Ctl* ctl) {
     __shared__ float red[kLnThreads / 32];
     griddep_wait();
     griddep_launch_dependents();
+    if (ctl != nullptr && __ldcg(&ctl->status) != 0) return;
     const size_t row = (size_t)blockIdx.x * d_h;
     const T* yr = y + row;
     const T* xr = x + row;
@@ -113,11 +117,12 @@ __device__ __forceinline__ void ln_store_chunk(float* p, const float (&f)[4]) {
 template <typename T>
 __global__ void __launch_bounds__(kLnThreads) residual_layernorm_vec_kernel(
     const T* y, const T* x, const float* __restrict__ ln_gamma, const float* __restrict__ ln_beta, float eps,
-    int d_h, T* out) {
+    int d_h, T* out, const Ctl* ctl) {
     constexpr int V = LnVec<T>::V;
     __shared__ float red[kLnThreads / 32];
     griddep_wait();
     griddep_launch_dependents();
+    const int status = ctl != nullptr ? __ldcg(&ctl->status) : 0;
     const size_t row = (size_t)blockIdx.x * d_h;
     const int nch = d_h / V;
     float v[kLnChunks][V];
@@ -136,6 +141,7 @@ __global__ void __launch_bounds__(kLnThreads) residual_layernorm_vec_kernel(
             }
         }
     }
+    if (status != 0) return;
     const float mu = ln_block_sum(s, red) / (float)d_h;
     float q = 0.f;
 #pragma unroll
@@ -166,7 +172,8 @@ __global__ void __launch_bounds__(kLnThreads) residual_layernorm_vec_kernel(
 static bool ln_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 cudaError_t launch_residual_layernorm(const void* y, const void* x, const float* ln_gamma, const float* ln_beta,
-                                      float eps, int T, int d_h, bool bf16, void* out, cudaStream_t s) {
+                                      float eps, int T, int d_h, bool bf16, void* out, cudaStream_t s,
+                                      const Ctl* ctl) {
     if (T == 0) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)T);
@@ -185,17 +192,18 @@ cudaError_t launch_residual_layernorm(const void* y, const void* x, const float*
     if (vec && bf16)
         return cudaLaunchKernelEx(&cfg, residual_layernorm_vec_kernel<__nv_bfloat16>,
                                   static_cast<const __nv_bfloat16*>(y), static_cast<const __nv_bfloat16*>(x),
-                                  ln_gamma, ln_beta, eps, d_h, static_cast<__nv_bfloat16*>(out));
+                                  ln_gamma, ln_beta, eps, d_h, static_cast<__nv_bfloat16*>(out), ctl);
     if (vec)
         return cudaLaunchKernelEx(&cfg, residual_layernorm_vec_kernel<float>, static_cast<const float*>(y),
                                   static_cast<const float*>(x), ln_gamma, ln_beta, eps, d_h,
-                                  static_cast<float*>(out));
+                                  static_cast<float*>(out), ctl);
     if (bf16)
         return cudaLaunchKernelEx(&cfg, residual_layernorm_kernel<__nv_bfloat16>,
                                   static_cast<const __nv_bfloat16*>(y), static_cast<const __nv_bfloat16*>(x),
-                                  ln_gamma, ln_beta, eps, d_h, static_cast<__nv_bfloat16*>(out));
+                                  ln_gamma, ln_beta, eps, d_h, static_cast<__nv_bfloat16*>(out), ctl);
     return cudaLaunchKernelEx(&cfg, residual_layernorm_kernel<float>, static_cast<const float*>(y),
-                              static_cast<const float*>(x), ln_gamma, ln_beta, eps, d_h, static_cast<float*>(out));
+                              static_cast<const float*>(x), ln_gamma, ln_beta, eps, d_h, static_cast<float*>(out),
+                              ctl);
 }
 
 }  // namespace bffn

@@ -386,3 +386,28 @@ def test_calls_after_an_error_leave_y(T, d_h, E, d_e):
     assert bffn.device_status(ws) == (4, 6) and torch.all(y == 9)
     ws.reset()
     assert torch.equal(bffn.forward_int8(*c, workspace=ws), good) and bffn.device_status(ws) == (0, 0)
+
+
+@pytest.mark.parametrize("d_h", [256, 8320])
+def test_layernorm_after_an_error_leaves_y(d_h):
+    """A refused call with a LayerNorm rewrites no row of y (rows in registers, and longer ones)."""
+    bffn = require_cuda()
+    T, E, d_e = 40, 4, 128
+    d = make(T, d_h, E, d_e, 5, 0.5)
+    c = [d[0].cuda()] + [torch.from_numpy(a).cuda() for a in d[1:6]]
+    ln = dict(ln_weight=torch.rand(d_h).cuda(), ln_bias=torch.rand(d_h).cuda())
+    ws = bffn.Workspace.for_forward_int8(T, d_h, E, d_e)
+    good = bffn.forward_int8(*c, workspace=ws, **ln)
+    assert torch.equal(good, bffn.residual_layernorm(bffn.forward_int8(*c), c[0], ln["ln_weight"], ln["ln_bias"]))
+    torch.cuda.synchronize()
+    y = torch.full_like(good, 9.0)
+    for key in (False, True):
+        ws.reset()
+        if key:
+            ws.buf[24] = 1                                # (the key of another form's shapes)
+        else:
+            ws.buf[:8] = torch.tensor([4, 0, 0, 0, 6, 0, 0, 0], dtype=torch.uint8)
+        bffn.forward_int8(*c, y=y, workspace=ws, **ln)
+        assert bffn.device_status(ws) == ((5, 10) if key else (4, 6)) and torch.all(y == 9)
+    ws.reset()
+    assert torch.equal(bffn.forward_int8(*c, workspace=ws, **ln), good)
