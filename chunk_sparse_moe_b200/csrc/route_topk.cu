@@ -418,7 +418,8 @@ __device__ __forceinline__ bool tk_choose(const TkArgs& a, const float (&z)[NJ],
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) key[j] = z[j] > -INFINITY ? K::of(z[j]) : typename K::Bits(0);
+        for (int j = 0; j < NJ; ++j)   // (adding 0 makes -0 a +0: equal logits have equal keys)
+            key[j] = z[j] > -INFINITY ? K::of(z[j] + 0.f) : typename K::Bits(0);
     }
     if constexpr (sizeof(typename K::Bits) == 4) {
         if (scored && !close && !tk_pick_quick<NJ>(a, lane, key, my_id)) return false;

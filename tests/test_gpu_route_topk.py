@@ -202,3 +202,24 @@ def test_refusals():
         bffn.route_topk_backward(z, ids.long(), w)
     with pytest.raises(ValueError):
         bffn.route_topk_backward(z, ids, w[:, :1])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+def test_zeros_of_either_sign_tie(scores, dtype):
+    """-0 and +0 are one logit: the lowest index goes first, also at the border of the choice."""
+    bffn = require_cuda()
+    E = 40
+    z = logits_of(8, E, dtype, 4)
+    z[0] = torch.where(torch.arange(E) % 2 == 0, -0.0, 0.0)
+    z[1] = -0.0
+    z[2] = torch.where(torch.arange(E) < 30, -0.0, 0.0)
+    z[3] = torch.where(z[3] > 0.5, torch.tensor(0.0, dtype=dtype), -z[3].abs() * (torch.arange(E) % 3 > 0))
+    z[4, :5], z[4, 5:] = -0.0, -1.0
+    z[5] = -z[5].abs()
+    z[5, ::7] = torch.tensor([0.0, -0.0, 0.0, -0.0, -0.0, 0.0])
+    assert torch.signbit(z[3]).logical_and(z[3] == 0).any() and (z[3] == 0).sum() > 6
+    for kw in (dict(), dict(bias=torch.zeros(E)), dict(bias=-torch.zeros(E), n_group=5, topk_group=2)):
+        _, ids, _ = check(bffn, z, 6, scores=scores, **kw)
+        if not kw:
+            assert all(list(r) == [0, 1, 2, 3, 4, 5] for r in ids[:3])
