@@ -537,8 +537,11 @@ __global__ void __launch_bounds__(kTkWarps * 32) route_topk_backward_kernel(
         if (id >= 0) {
             dw = d_weights[(size_t)t * k + lane] * scale;
             zi = tk_f32(row[id]);
-            zi = fminf(zi, FLT_MAX);
-            if (!(zi > -INFINITY)) id = -1;   // an expert that cannot be chosen has no weight
+            zi = zi == zi ? fminf(zi, FLT_MAX) : -INFINITY;   // (as the forward reads it)
+            if (!(zi > -INFINITY)) {   // an expert that cannot be chosen has no weight
+                id = -1;
+                dw = 0.f;
+            }
         }
     }
     const bool have = id >= 0;

@@ -175,8 +175,9 @@ blockffn_status blockffn_route_topk(const void* logits, blockffn_dtype dt, const
  * logits [T, E] in dt and ids [T, k] as given to and returned by blockffn_route_topk;
  * d_weights [T, k] fp32 (where the gradient of the dense gates is at hand, its values
  * at ids); scores, renormalize and scale as in the forward; d_logits [T, E] in dt,
- * fully overwritten.  An id outside [0, E) has no gradient (its d_weights is not read
- * into the result); an id listed twice counts twice.
+ * fully overwritten.  An id outside [0, E), or of an expert that cannot be chosen (its
+ * logit -infinity or NaN), has no gradient and its d_weights is not read into the
+ * result; an id listed twice counts twice.
  */
 blockffn_status blockffn_route_topk_backward(const void* logits, blockffn_dtype dt, const int32_t* ids,
                                              const float* d_weights, int T, int E, int k,

@@ -223,3 +223,26 @@ def test_zeros_of_either_sign_tie(scores, dtype):
         _, ids, _ = check(bffn, z, 6, scores=scores, **kw)
         if not kw:
             assert all(list(r) == [0, 1, 2, 3, 4, 5] for r in ids[:3])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_backward_of_ids_that_cannot_be_chosen(renorm, scores, dtype):
+    """Ids whose logit is NaN or -inf have no weight: no gradient from them, whatever their d_weights hold, and
+    the others' as if they were not listed."""
+    bffn = require_cuda()
+    E, k = 40, 5
+    z = logits_of(6, E, dtype, 6)
+    ids = torch.tensor([[3, 7, 9, 11, 2]] * 6, dtype=torch.int32)
+    dw = torch.from_numpy(np.random.default_rng(1).standard_normal((6, k)).astype(np.float32))
+    z[0, 7], z[1, 3], z[1, 2] = float("nan"), float("nan"), -INF
+    z[2, 9], dw[2, 2] = float("nan"), float("nan")
+    z[3, 11], dw[3, 3] = -INF, INF
+    z[4] = float("nan")
+    z[5, 30:] = float("nan")               # (not among the ids)
+    got = bffn.route_topk_backward(z.cuda(), ids.cuda(), dw.cuda(), scores=scores, renormalize=renorm, scale=2.0)
+    want, size = ref.backward(z.double().numpy(), ids.numpy(), dw.numpy(), scores, renorm, 2.0)
+    assert np.all(np.isfinite(want)) and not np.any(want[4]) and np.any(want[0])
+    tol = 3 * W_TOL * size + torch.finfo(dtype).eps / 2 * np.abs(want) * 1.01 + 1e-37
+    assert np.all(np.abs(got.double().cpu().numpy() - want) <= tol)
