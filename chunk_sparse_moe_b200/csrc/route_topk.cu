@@ -202,6 +202,16 @@ __device__ __forceinline__ void tk_choice_keys(const TkArgs& a, const float (&z)
     }
 }
 
+// How much larger the two parts of a group's value are than the value itself (0 unless their
+// signs differ): their rounding stays while they cancel, so the doubtful gap grows with the
+// most of it in any group.
+__device__ __forceinline__ float tk_cancelled(float v1, float v2) {
+    return (v1 > 0.f) != (v2 > 0.f) ? 2.f * fminf(fabsf(v1), fabsf(v2)) : 0.f;
+}
+__device__ __forceinline__ float tk_warp_most(float v) {   // (of numbers >= 0)
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
+}
+
 // tk_keep_groups for groups that are whole lanes, a power of two of them (32 / n_group, as with
 // 32 NJ experts in a power of two of groups): the two largest keys of a group meet in
 // butterflies.  Same result.
@@ -221,8 +231,13 @@ __device__ __forceinline__ bool tk_keep_lane_groups(const TkArgs& a, int lane, u
     }
     // the group's value, in its first lane
     uint32_t gv = 0;
-    if (b1 != 0 && (lane & (L - 1)) == 0)
-        gv = Key32::of(Key32::value(b1) + (b2 != 0 ? Key32::value(b2) : 0.f));
+    float lost = 0.f;
+    if (b1 != 0 && (lane & (L - 1)) == 0) {
+        const float v1 = Key32::value(b1), v2 = b2 != 0 ? Key32::value(b2) : 0.f;
+        gv = Key32::of(v1 + v2);
+        lost = tk_cancelled(v1, v2);
+    }
+    lost = tk_warp_most(lost);
     uint32_t kept = 0;   // lanes of the kept groups
     const uint32_t lanes = L == 32 ? 0xffffffffu : (1u << L) - 1u;
     float last = 0.f;
@@ -232,7 +247,7 @@ __device__ __forceinline__ bool tk_keep_lane_groups(const TkArgs& a, int lane, u
         if (m == 0) break;
         const float v = Key32::value(m);
         if (n == a.topk_group) {
-            close = last - v <= 8e-6f * (1.f + fabsf(v));
+            close = !(last - v > 8e-6f * (1.f + fabsf(v) + lost));
             break;
         }
         const int src = __ffs(__ballot_sync(0xffffffffu, gv == m)) - 1;
@@ -261,6 +276,7 @@ __device__ __forceinline__ bool tk_keep_groups(const TkArgs& a, int lane, typena
     __syncwarp();
     constexpr int kMaxPerLane = kTkMaxE / 32;
     Bits gv[kMaxPerLane];
+    float lost = 0.f;
     const int G = a.n_group, per = a.per;
 #pragma unroll
     for (int i = 0; i < kMaxPerLane; ++i) {
@@ -273,9 +289,14 @@ __device__ __forceinline__ bool tk_keep_groups(const TkArgs& a, int lane, typena
                 b2 = v > b1 ? b1 : (v > b2 ? v : b2);
                 b1 = v > b1 ? v : b1;
             }
-            if (b1 != 0) gv[i] = K::of(K::value(b1) + (b2 != 0 ? K::value(b2) : R(0)));
+            if (b1 != 0) {
+                const R v1 = K::value(b1), v2 = b2 != 0 ? K::value(b2) : R(0);
+                gv[i] = K::of(v1 + v2);
+                lost = fmaxf(lost, tk_cancelled((float)v1, (float)v2));
+            }
         }
     }
+    lost = tk_warp_most(lost);
     uint32_t kept = 0;    // bit i: group lane + 32 i is kept
     bool close = false;
     R last = R(0);
@@ -289,7 +310,7 @@ __device__ __forceinline__ bool tk_keep_groups(const TkArgs& a, int lane, typena
         if (m == 0) break;
         const R v = K::value(m);
         if (n == a.topk_group) {
-            close = last - v <= R(8e-6f) * (R(1) + fabs(v));
+            close = !(last - v > R(8e-6f) * (R(1) + fabs(v) + R(lost)));
             break;
         }
         // lowest index of a tie: lowest i first, then the lowest lane

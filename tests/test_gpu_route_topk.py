@@ -246,3 +246,24 @@ def test_backward_of_ids_that_cannot_be_chosen(renorm, scores, dtype):
     assert np.all(np.isfinite(want)) and not np.any(want[4]) and np.any(want[0])
     tol = 3 * W_TOL * size + torch.finfo(dtype).eps / 2 * np.abs(want) * 1.01 + 1e-37
     assert np.all(np.abs(got.double().cpu().numpy() - want) <= tol)
+
+
+@pytest.mark.parametrize("E,G,g", [(64, 8, 3), (60, 6, 2), (256, 32, 9)])
+def test_groups_whose_two_best_cancel(E, G, g):
+    """Biases of a few hundred of either sign: a group's value is the small difference of two large scores, whose
+    fp32 rounding (1.5e-5 at 200) is far above the gaps between groups.  The choice is that of 64 bits."""
+    bffn = require_cuda()
+    rng = np.random.default_rng(E)
+    T, per = 300, E // G
+    z = torch.from_numpy((0.02 * rng.standard_normal((T, E))).astype(np.float32))
+    bias = torch.full((E,), -1000.0)
+    size = torch.from_numpy(rng.integers(150, 400, G).astype(np.float32))
+    for i in range(G):                     # its two best: +size and -size, and the scores
+        bias[i * per + int(rng.integers(0, per // 2))] = size[i]
+        bias[i * per + int(rng.integers(per // 2, per))] = -size[i]
+    for scores in ("softmax", "sigmoid"):
+        check(bffn, z, 3, scores=scores, bias=bias, n_group=G, topk_group=g)
+        # and one group alone that cancels, far above the others' border or next to it
+        one = 0.2 * torch.from_numpy(rng.standard_normal(E).astype(np.float32))
+        one[:per] = bias[:per]
+        check(bffn, z, 3, scores=scores, bias=one, n_group=G, topk_group=g)
