@@ -165,11 +165,10 @@ struct TkArgs {
     float* weights;        // [T, k]
 };
 
-// Keys of the choice from the logits, in K::Real arithmetic; *m and *sum (softmax)
-// come back for the weights.
+// Keys of the choice from the logits (softmax: the largest is m), in K::Real arithmetic.
 template <int NJ, class K>
 __device__ __forceinline__ void tk_choice_keys(const TkArgs& a, const float (&z)[NJ], const float* brow, int lane,
-                                               typename K::Bits (&key)[NJ], float& m, float& sum) {
+                                               typename K::Bits (&key)[NJ], float m) {
     using R = typename K::Real;
     R s[NJ];
     if (a.sigmoid) {
@@ -183,7 +182,6 @@ __device__ __forceinline__ void tk_choice_keys(const TkArgs& a, const float (&z)
             part += s[j];
         }
         const R total = tk_warp_sum(part);
-        sum = (float)total;
         const R inv = total > R(0) ? R(1) / total : R(0);
 #pragma unroll
         for (int j = 0; j < NJ; ++j) s[j] *= inv;
@@ -424,11 +422,11 @@ __device__ __forceinline__ bool tk_pick_quick(const TkArgs& a, int lane, const u
 
 template <int NJ, class K>
 __device__ __forceinline__ bool tk_choose(const TkArgs& a, const float (&z)[NJ], int lane, void* srow, bool scored,
-                                          int& my_id, float& m, float& sum) {
+                                          int& my_id, float m) {
     typename K::Bits key[NJ];
     bool close = false;
     if (scored) {
-        tk_choice_keys<NJ, K>(a, z, a.bias, lane, key, m, sum);
+        tk_choice_keys<NJ, K>(a, z, a.bias, lane, key, m);
         if (a.n_group > 1) {
             if constexpr (sizeof(typename K::Bits) == 4) {
                 if (a.lane_groups) close = tk_keep_lane_groups<NJ>(a, lane, key);
@@ -474,7 +472,7 @@ __global__ void __launch_bounds__(kTkWarps * 32) route_topk_kernel(const T* __re
         }
         mk = Key32::warp_max(mk);
         m = mk != 0 ? Key32::value(mk) : 0.f;
-        if (!scored) {
+        if (!a.renorm) {   // (not the choice's sum: the same logits have the same weights however they are chosen)
             float part = 0.f;
 #pragma unroll
             for (int j = 0; j < NJ; ++j) part += z[j] > -INFINITY ? expf(z[j] - m) : 0.f;
@@ -482,8 +480,8 @@ __global__ void __launch_bounds__(kTkWarps * 32) route_topk_kernel(const T* __re
         }
     }
     int id;
-    if (tk_choose<NJ, Key32>(a, z, lane, stage[warp], scored, id, m, sum))
-        tk_choose<NJ, Key64>(a, z, lane, stage[warp], scored, id, m, sum);
+    if (tk_choose<NJ, Key32>(a, z, lane, stage[warp], scored, id, m))
+        tk_choose<NJ, Key64>(a, z, lane, stage[warp], scored, id, m);
 
     // weights, in lane i for the i-th choice
     const bool have = id >= 0;

@@ -267,3 +267,21 @@ def test_groups_whose_two_best_cancel(E, G, g):
         one = 0.2 * torch.from_numpy(rng.standard_normal(E).astype(np.float32))
         one[:per] = bias[:per]
         check(bffn, z, 3, scores=scores, bias=one, n_group=G, topk_group=g)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,E,k", [(300, 256, 8), (300, 60, 6), (7, 32, 3)])
+def test_plain_softmax_weights_do_not_depend_on_how_they_are_chosen(T, E, k, dtype):
+    """A bias of zeros and groups that hold the chosen experts anyway change no bit of the weights."""
+    bffn = require_cuda()
+    z = logits_of(T, E, dtype, T + E, spread=4.0).cuda()
+    want = bffn.route_topk(z, k, renormalize=False, scale=1.5)
+    zero = torch.zeros(E, device="cuda")
+    for kw in (dict(bias=zero), dict(bias=zero, n_group=2, topk_group=2)):
+        got = bffn.route_topk(z, k, renormalize=False, scale=1.5, **kw)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    gates, ids, w = bffn.route_topk(z, k, renormalize=False, scale=1.5, n_group=4, topk_group=2)
+    full = bffn.route_topk(z, min(32, E), renormalize=False, scale=1.5)[0]
+    # the same experts' weights among the min(32, E) largest, where they are there
+    listed = full.gather(1, ids.long())
+    assert (listed != 0).float().mean() > 0.5 and torch.all((listed == 0) | (listed == w))
