@@ -379,7 +379,17 @@ def forward_int8(x: torch.Tensor, gates: torch.Tensor, W_in: torch.Tensor, s_in:
 
 
 def device_status(workspace: Workspace):
-    """(status, detail) of the workspace's device status word (synchronizes the stream)."""
+    """(status, detail) of the workspace's device status word (synchronizes the current stream of the
+    workspace's device)."""
     detail = ctypes.c_int32(0)
-    st = lib.blockffn_get_device_status(workspace.buf.data_ptr(), _stream(), ctypes.byref(detail))
+    device = workspace.buf.device
+
+    def read() -> int:
+        return lib.blockffn_get_device_status(workspace.buf.data_ptr(), _stream(), ctypes.byref(detail))
+
+    if device.index == torch.cuda.current_device():
+        st = read()
+    else:
+        with torch.cuda.device(device):
+            st = read()
     return int(st), int(detail.value)
