@@ -796,7 +796,7 @@ blockffn_status blockffn_forward(const void* x, const float* gates, const void* 
         e = launch_expert_bias_sum(g, t_counts, t_idx, t_tmask, ctl, b_out, T, d_h, E, n, ybias, s);
         if (e != cudaSuccess) return cuda_fail(e, "expert bias launch");
     }
-    CUtensorMap maps[6];
+    CUtensorMap maps[5];
     // expert-out partial tiles [blocks][2 slots][N/4 token quads][128 rows x 4 tokens]
     // fp32, seen as lines of 512 floats; a box is 32 rows of every token quad
     if (!make_map(&maps[0], x, (uint64_t)d_h, (uint64_t)T, (uint32_t)L.N) ||
