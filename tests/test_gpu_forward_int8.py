@@ -411,3 +411,30 @@ def test_layernorm_after_an_error_leaves_y(d_h):
         assert bffn.device_status(ws) == ((5, 10) if key else (4, 6)) and torch.all(y == 9)
     ws.reset()
     assert torch.equal(bffn.forward_int8(*c, workspace=ws, **ln), good)
+
+
+@pytest.mark.parametrize("T,d_h,E,d_e", [(256, 128, 256, 128), (600, 128, 256, 128)])
+def test_every_gate_on_with_256_experts(T, d_h, E, d_e):
+    """The fullest list of work that a block of the last step can have: 256 tokens of all 256 experts."""
+    bffn = require_cuda()
+    d = make(T, d_h, E, d_e, 8, 1.0)
+    ws = bffn.Workspace.for_forward_int8(T, d_h, E, d_e)
+    y = call(bffn, d, workspace=ws)
+    assert bffn.device_status(ws) == (0, 0)
+    compare(y, d)
+
+
+@pytest.mark.parametrize("T,d_h,E,d_e,biases", [(700, 512, 64, 128, True), (3000, 256, 64, 128, False)])
+def test_long_input_with_gates_of_a_relu_router(T, d_h, E, d_e, biases):
+    """About a fifth of the experts a token, neighbours alike, some tokens with none."""
+    bffn = require_cuda()
+    rng = np.random.default_rng(T)
+    d = list(make(T, d_h, E, d_e, T, 0.0, biases))
+    runs = np.repeat(rng.random(((T + 7) // 8, E)) < 0.22, 8, 0)[:T]
+    on = runs & (rng.random((T, E)) < 0.9) & (rng.random((T, 1)) >= 0.05)
+    d[1] = np.where(on, np.abs(rng.standard_normal((T, E))), 0).astype(np.float32)
+    assert not on.any(1).all()
+    ws = bffn.Workspace.for_forward_int8(T, d_h, E, d_e)
+    y = call(bffn, d, workspace=ws)
+    assert bffn.device_status(ws) == (0, 0)
+    compare(y, d)
