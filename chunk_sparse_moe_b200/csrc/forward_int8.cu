@@ -224,23 +224,15 @@ __device__ __forceinline__ float xi_swish(float z) {
     return d < INFINITY ? fmaf(fmaf(-q, d, z), r, q) * 0.125f : q;
 }
 
-// The whole number q next to 127 h / amax put right where it may be the one on the other side of
-// a border: 127 h - q amax is exact in 64 bits (31 bits each), so what comes out is rint of the
-// exact quotient.
-__device__ __noinline__ float xi_border(float h, float amax, float q) {
-    const double d = 127.0 * (double)h - (double)q * (double)amax, half = 0.5 * (double)amax;
-    if (fabs(d) > half || (fabs(d) == half && ((int)q & 1))) q += d > 0.0 ? 1.f : -1.f;
-    return q;
-}
-
 // What the epilogue does with PW columns (tokens) of int32 sums: h, its scale over all of
 // d_e (the four warps of the group meet in colmax), 8-bit h and the pair's factors.  Lane i
 // (of PW) holds column i's token, its scale and gate, and the place of the pair in the
 // expert's list (slot, -1: no pair); pair0: the list's first pair.
-// z and Swish go to fp32's last bit or two, and the rounding to 8 bits is decided again near the
-// border of two whole numbers: a value on the wrong side moves its token's whole row of y.
-// (From the approximate exponential and quotient alone that was one value in 700000, and h
-// was 0 below z = -87.)
+// z, Swish and 127 h / amax are evaluated as the formula reads, every step rounded once to fp32
+// (near the border of two whole numbers, that is; elsewhere h * (127 / amax) rounds to the same
+// number): a value on the other side of a border moves its token's whole row of y.  (From the
+// approximate exponential and quotient alone that was one value in 700000, and h was 0 below
+// z = -87.)
 template <int MT, int PW>
 __device__ __forceinline__ void xi_finish(const X8In& a, XiShared& sh, const int (&v)[MT][PW], size_t pair0, int slot,
                                           int token, float sx, float gate, const float (&si)[MT],
@@ -270,8 +262,8 @@ __device__ __forceinline__ void xi_finish(const X8In& a, XiShared& sh, const int
         a.w.pair[pair0 + slot] = make_float4(__int_as_float(token), gate * r.scale, gate, 0.f);
     int8_t* out = a.w.hq + pair0 * a.d_e + q * 32 + lane;
     // rounded by adding 1.5 * 2^23 (the whole number is the sum's low byte); what was rounded off
-    // is off by 127 * 2^-24 at most, inv's share
-    constexpr float kMagic = 12582912.f, kNear = 0.49998f;
+    // is off by 127 * 2^-24 at most, inv's share, and the formula's own steps by twice that
+    constexpr float kMagic = 12582912.f, kNear = 0.49997f;
     float worst = 0.f;
 #pragma unroll
     for (int i = 0; i < PW; ++i) {
@@ -296,7 +288,8 @@ __device__ __forceinline__ void xi_finish(const X8In& a, XiShared& sh, const int
                 for (int mt = 0; mt < MT; ++mt) {
                     const float t = fmaf(h[mt][i], inv, kMagic);
                     if (fabsf(fmaf(h[mt][i], inv, kMagic - t)) > kNear)
-                        out[(size_t)at * a.d_e + mt * 128] = (int8_t)(int)xi_border(h[mt][i], amax, t - kMagic);
+                        out[(size_t)at * a.d_e + mt * 128] =
+                            (int8_t)(int)rintf(__fdiv_rn(__fmul_rn(h[mt][i], 127.f), amax));
                 }
             }
         }

@@ -332,9 +332,10 @@ blockffn_status blockffn_forward(const void* x, const float* gates, const void* 
  *   h        = Swish(z);  (hq, sh) = h rounded to 8 bits, one scale over the d_e values
  *   y[t,o]  += gates[t,e] (sh s_out[e,o] sum_j hq[j] W_out[e,o,j] + (b_out ? b_out[e,o] : 0))
  * then y <- LayerNorm(y + x) when opts->ln_weight is given.  The integer sums are exact
- * (int32); z and Swish are fp32, each step within its last bit or two, and hq is the exact
- * rounding of them, halves to even (below z = -88.7 h counts as 0); the sum over experts is
- * fp32 in a fixed order and is rounded once to dt.
+ * (int32).  z (two products, then the bias), z / (1 + exp(-z)) and the 127 h / max|h| that
+ * hq rounds, halves to even, are evaluated step by step in fp32 (below z = -88.7, where
+ * exp(-z) passes its range, h is 0); the sum over experts is fp32 in a fixed order and is
+ * rounded once to dt.
  * The chunk length plays no part: an expert is computed for the tokens that use it.
  *
  * x, y [T, d_h] bf16 (dt must be BLOCKFFN_BF16); gates [T, E] fp32; W_in [E, d_e, d_h]
