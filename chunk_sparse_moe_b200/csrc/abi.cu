@@ -557,6 +557,12 @@ blockffn_status blockffn_forward_int8(const void* x, const float* gates, const i
         !aligned16(s_out) || !aligned16(y) || !aligned16(workspace) || (b_in && !aligned16(b_in)) ||
         (b_out && !aligned16(b_out)) || (ln_w && !aligned16(ln_w)) || (ln_b && !aligned16(ln_b)))
         return fail(BLOCKFFN_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
+    if (ln_w) {
+        const uintptr_t xa = reinterpret_cast<uintptr_t>(x), ya = reinterpret_cast<uintptr_t>(y);
+        const uintptr_t bytes = (uintptr_t)T * d_h * 2;
+        if (xa < ya + bytes && ya < xa + bytes)
+            return fail(BLOCKFFN_ERR_INVALID_ARG, "y may not overlap x when a LayerNorm follows");
+    }
     const X8Layout L = x8_layout(T, d_h, E, d_e);
     if (ws_bytes < L.total)
         return fail(BLOCKFFN_ERR_WORKSPACE, "workspace of %zu bytes < %zu needed", ws_bytes, L.total);

@@ -341,9 +341,10 @@ blockffn_status blockffn_forward(const void* x, const float* gates, const void* 
  * x, y [T, d_h] bf16 (dt must be BLOCKFFN_BF16); gates [T, E] fp32; W_in [E, d_e, d_h]
  * and W_out [E, d_h, d_e] int8 with channel scales s_in [E, d_e] and s_out [E, d_h]
  * fp32; opts as in blockffn_forward.  y is fully overwritten (zeros for a token with no
- * active expert, before a LayerNorm); it may be x itself when there is no LayerNorm.  A
- * token that holds an infinity or NaN, or an active gate that is one, gives a row that is
- * not finite and touches no other row.
+ * active expert, before a LayerNorm); it may be x itself when there is no LayerNorm (with
+ * one, a y that overlaps x is refused).  A token that holds an infinity or NaN and uses an
+ * expert, or an active gate that is one, gives a row that is not finite and touches no
+ * other row.
  * workspace: ws_bytes >= blockffn_forward_int8_workspace_bytes(T, d_h, E, d_e) (0 for
  * shapes that are refused), reset once before its first use; it holds nothing between
  * calls but the status word, so 8-bit calls of any shapes may share one that is large

@@ -100,3 +100,13 @@ def test_forward_int8_options_and_sizes(lib):
     # bounded by the slice: a long input needs no more than one of 8192 tokens
     assert f(100000, 256, 8, 128) == f(8192, 256, 8, 128) > f(100, 256, 8, 128) > 0
     assert L.blockffn_forward_int8(*{**FORWARD, "T": 0, "x": None, "y": None, "ws": None}.values()) == lib.OK
+
+
+@pytest.mark.parametrize("y", [1 << 20, (1 << 20) + 64, (1 << 20) - 1024])
+def test_forward_int8_refuses_a_y_over_x_with_a_layernorm(lib, y):
+    """The LayerNorm reads x after y has been written, so the two may not share memory then."""
+    import ctypes
+    o = lib.LayerOpts(None, None, 16, None, 1e-5)
+    call = {**FORWARD, "x": 1 << 20, "y": y, "opts": ctypes.byref(o)}   # (4 x 256 bf16: 2048 bytes)
+    assert lib.lib.blockffn_forward_int8(*call.values()) == lib.ERR_INVALID_ARG
+    assert b"LayerNorm" in lib.lib.blockffn_last_error_message()
