@@ -439,3 +439,33 @@ def test_long_input_with_gates_of_a_relu_router(T, d_h, E, d_e, biases):
     y = call(bffn, d, workspace=ws)
     assert bffn.device_status(ws) == (0, 0)
     compare(y, d)
+
+
+@pytest.mark.parametrize("T", [4, 700])
+def test_calls_at_once_on_two_streams(T):
+    """The three steps of a layer on two streams at once, each with its own workspaces: the bits of a call alone."""
+    bffn = require_cuda()
+    d_h, E, d_e = 512, 32, 128
+    sets = []
+    for seed in (1, 2):
+        d = make(T, d_h, E, d_e, seed, 0.2)
+        c = [d[0].cuda()] + [torch.from_numpy(a).cuda() for a in d[1:6]]
+        W = torch.from_numpy(np.random.default_rng(seed).integers(-127, 128, (E, d_h)).astype(np.int8)).cuda()
+        ws = (bffn.Workspace.for_int8_linear(T, d_h, E), bffn.Workspace.for_forward_int8(T, d_h, E, d_e))
+        sets.append((c, W, torch.rand(E).cuda() / 500, ws, torch.cuda.Stream()))
+
+    def layer(c, W, s, ws):
+        gates, ids, w = bffn.route_topk(bffn.int8_linear(c[0], W, s, out_dtype=torch.float32, workspace=ws[0]), 4)
+        return ids, w, bffn.forward_int8(c[0], gates, *c[2:], workspace=ws[1])
+
+    want = [layer(*s[:4]) for s in sets]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(40):
+        for i, s in enumerate(sets):
+            with torch.cuda.stream(s[4]):
+                got[i].append(layer(*s[:4]))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert all(torch.equal(a, b) for g in got[i] for a, b in zip(g, want[i]))
+        assert all(bffn.device_status(ws) == (0, 0) for ws in sets[i][3])
