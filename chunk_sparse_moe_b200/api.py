@@ -252,7 +252,8 @@ def route_topk(logits: torch.Tensor, k: int, scores: str = "softmax", bias: Opti
     chosen scores without the bias, divided by their sum when ``renormalize`` is set,
     times ``scale``.  ``gates`` holds them densely, as ``chunk_union`` and the forwards
     take them.  Ties go to the lowest index; an expert whose logit is -inf is never
-    chosen (ids -1 and weight 0 where too few are left).  ``out``: the three outputs."""
+    chosen (ids -1 and weight 0 where too few are left).  ``out``: the three outputs.
+    No call of the package records a gradient: ``route_topk_backward`` gives this one's."""
     T, E = logits.shape
     dev = logits.device
     if bias is not None:

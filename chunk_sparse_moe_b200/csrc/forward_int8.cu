@@ -35,11 +35,13 @@
 //
 // What bounds them.  Decode: the way through three dependent launches, each with a plan
 // to read: at d_h 2048, 8 of 64 experts, 15 us for one token and 19.5 us for a 32-token
-// chunk, whose bytes take 0.7 and 3.4 us.  Long inputs (114 us at 4096 tokens; the three
-// kernels alone 11, 31 and 80 us, the bytes and the products 10.6 us each): in
-// experts_out the sums' read-modify-write in shared memory, 8 bytes for every pair and
-// channel (57 % of the shared-memory pipe, 6 % of the tensor pipe, 1.73 waves
-// of blocks).  Tried there and slower: entries in twos under
+// chunk, whose bytes take 0.7 and 3.4 us.  Long inputs (117 us at 4096 tokens; the three
+// kernels alone 12, 36 and 81 us, the bytes and the products 10.6 us each): the entries of
+// experts_out, one expert's pairs in a tile of tokens.  A block takes some 1200 cycles for one of
+// about 32 pairs, of which the sums' read-modify-write in shared memory, 8 bytes for every
+// pair and channel, is 256 (57 % of the shared-memory pipe, 6 % of the tensor pipe; 256 blocks
+// are 1.73 waves); the time follows the number of entries more than that of pairs.  Tried there
+// and slower: entries in twos under
 // one barrier with their pieces pipelined (118 -> 123 us), four epilogue groups instead
 // of two (118 -> 123 us), 128-token tiles (142 -> 198 us: twice the entries).
 #include <cuda.h>

@@ -151,11 +151,12 @@ typedef enum {
  *            times scale.  The bias takes part in the choice only.
  *   gates[t, :] = 0 except gates[t, ids[i]] = w[i]
  *
- * Ties go to the lowest expert (group) index; the choice is that of the exact
- * scores, not of rounded ones.  logits [T, E] in dt.  An expert whose logit (or
- * bias) is -infinity or NaN is never chosen; +infinity counts as the largest
- * finite value.  A token with fewer than k choosable experts in its groups has
- * ids -1 and weights 0 at the end of its list (a fully masked one: everywhere).
+ * Ties go to the lowest expert (group) index (-0 and +0 are one logit); the choice is
+ * that of scores in 64 bits, and of the logits themselves without bias and groups.
+ * logits [T, E] in dt.  An expert whose logit (or bias) is -infinity or NaN is never
+ * chosen; +infinity counts as the largest finite value.  A token with fewer than k
+ * choosable experts in its groups has ids -1 and weights 0 at the end of its list (a
+ * fully masked one: everywhere).
  * A gate can be an exact zero where its score underflows; such an expert is
  * listed in ids but not active for the forwards.
  * Outputs: gates [T, E] fp32 or NULL, ids [T, k] int32, weights [T, k] fp32.
